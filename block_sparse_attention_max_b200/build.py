@@ -14,8 +14,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libveda.so")
 
-SOURCES = ["veda_lib.cu", "veda_tile_map.cpp", "veda_plan.cpp"]
-HEADERS = ["veda_ptx.cuh", "k_attn.cuh", "k_heat.cuh", "k_bwd.cuh", "k_fp8.cuh", "k_gather.cuh", "k_scores.cuh", "k_select.cuh"]
+SOURCES = ["veda_lib.cu", "veda_norm.cu", "veda_tile_map.cpp", "veda_plan.cpp"]
+HEADERS = ["veda_ptx.cuh", "k_attn.cuh", "k_heat.cuh", "k_bwd.cuh", "k_fp8.cuh", "k_gather.cuh", "k_scores.cuh", "k_select.cuh",
+           "k_int8.cuh", "k_norm.cuh", "k_rotary.cuh", "veda_host.h"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -23,6 +24,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-warn-spills",
+    "--threads", "0",          # the two CUDA sources side by side
 ]
 
 

@@ -16,8 +16,11 @@
 #include "k_bwd.cuh"
 #include "k_fp8.cuh"
 #include "k_gather.cuh"
+#include "k_int8.cuh"
+#include "k_rotary.cuh"
 #include "k_scores.cuh"
 #include "k_select.cuh"
+#include "veda_host.h"
 #include "veda_ptx.cuh"
 
 namespace veda {
@@ -31,6 +34,7 @@ struct DeviceInfo {
   int sms = 0;
   bool attrs_set = false;
   int per_sm_copy = 1, per_sm_unpermute = 1, per_sm_pool = 1, per_sm_permpool = 1;   // resident CTAs per SM
+  int per_sm_rotpool[2] = {1, 1}, per_sm_rotback[2] = {1, 1};   // [half layout]
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -86,6 +90,9 @@ veda_status current_device(int& sms) {
         {reinterpret_cast<const void*>(bwd::bwd_kernel<bwd::kModeDKDV>), static_cast<int>(bwd::kSmemBytesDKDV)},
         {reinterpret_cast<const void*>(sgemm::nt_gemm_3xtf32_kernel), static_cast<int>(sgemm::kSmemBytes)},
         {reinterpret_cast<const void*>(select_kernel), static_cast<int>(kSelMaxSmem)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__nv_bfloat16>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__half>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float>), static_cast<int>(int8::kSmemBytes)},
     };
     for (auto& x : attrs) {
       e = cudaFuncSetAttribute(x.f, cudaFuncAttributeMaxDynamicSharedMemorySize, x.bytes);
@@ -110,12 +117,20 @@ veda_status current_device(int& sms) {
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_copy, permute_kernel, kCopyThreads, 0)) != cudaSuccess ||
         (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_unpermute, unpermute_kernel, kCopyThreads, 0)) != cudaSuccess ||
         (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_pool, pool_kernel, kPoolThreads, 0)) != cudaSuccess ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_permpool, permute_pool_kernel, kPoolThreads, 0)) != cudaSuccess)
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_permpool, permute_pool_kernel, kPoolThreads, 0)) != cudaSuccess ||
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotpool[0], rotary::rotary_permute_pool_kernel<false>, kPoolThreads, 0)) != cudaSuccess ||
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotpool[1], rotary::rotary_permute_pool_kernel<true>, kPoolThreads, 0)) != cudaSuccess ||
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotback[0], rotary::rotary_unpermute_kernel<false>, kCopyThreads, 0)) != cudaSuccess ||
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotback[1], rotary::rotary_unpermute_kernel<true>, kCopyThreads, 0)) != cudaSuccess)
       return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
     d.per_sm_copy = d.per_sm_copy < 1 ? 1 : d.per_sm_copy;
     d.per_sm_unpermute = d.per_sm_unpermute < 1 ? 1 : d.per_sm_unpermute;
     d.per_sm_pool = d.per_sm_pool < 1 ? 1 : d.per_sm_pool;
     d.per_sm_permpool = d.per_sm_permpool < 1 ? 1 : d.per_sm_permpool;
+    for (int i = 0; i < 2; ++i) {
+      d.per_sm_rotpool[i] = std::max(1, d.per_sm_rotpool[i]);
+      d.per_sm_rotback[i] = std::max(1, d.per_sm_rotback[i]);
+    }
     d.attrs_set = true;
   }
   sms = d.sms;
@@ -215,10 +230,65 @@ int grid_for(int64_t units, int sms, int per_sm) {
   return static_cast<int>(units < g ? units : g);
 }
 
+// 8-bit rows of kp bytes (a multiple of 16): box 128 bytes x box_rows, 128-byte swizzle. Bytes
+// past a row and rows past the end read as zero.
+veda_status encode_codes(CUtensorMap& m, const void* base, uint64_t kp, uint64_t rows, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {kp, rows};
+  const cuuint64_t strides[1] = {kp};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
+  return VEDA_OK;
+}
+
+bool known_type(int32_t dtype) { return dtype >= VEDA_BF16 && dtype <= VEDA_FP32; }
+int64_t type_size(int32_t dtype) { return dtype == VEDA_FP32 ? 4 : 2; }
+
+// Rotation arguments of the tile kernels; `call` names the entry in messages.
+veda_status check_tile_rotation(const char* call, const float* cos_sin, int64_t table_rows, int32_t rot_dim, int32_t B,
+                                int32_t N, int32_t D) {
+  const std::string c(call);
+  if (D != 128) return fail(VEDA_ERR_UNSUPPORTED, "head_dim must be 128");
+  if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16)
+    return fail(VEDA_ERR_UNSUPPORTED, c + ": rot_dim must be a multiple of 16 in [16, 128]");
+  if (!cos_sin || !aligned(cos_sin, 16)) return fail(VEDA_ERR_INVALID_ARG, c + ": cos_sin must be 16-byte aligned");
+  if (table_rows != N && table_rows != static_cast<int64_t>(B) * N)
+    return fail(VEDA_ERR_INVALID_ARG, c + ": the table has neither N nor B * N rows");
+  return VEDA_OK;
+}
+
 }  // namespace
+
+veda_status host_device(int& sms) { return current_device(sms); }
+
 }  // namespace veda
 
 using namespace veda;
+
+namespace {
+template <typename T>
+veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
+  if (p.M <= int8::kFewMax) {
+    const unsigned grid = static_cast<unsigned>((p.N + int8::kFewThreads / 32 - 1) / (int8::kFewThreads / 32));
+    if (p.M == 1) int8::few_tokens_kernel<T, 1><<<grid, int8::kFewThreads, 0, s>>>(p);
+    else if (p.M == 2) int8::few_tokens_kernel<T, 2><<<grid, int8::kFewThreads, 0, s>>>(p);
+    else if (p.M <= 4) int8::few_tokens_kernel<T, 4><<<grid, int8::kFewThreads, 0, s>>>(p);
+    else int8::few_tokens_kernel<T, 8><<<grid, int8::kFewThreads, 0, s>>>(p);
+    return launched("few_tokens_kernel");
+  }
+  veda_status st = get_encoder();
+  if (st != VEDA_OK) return st;
+  CUtensorMap mA, mB;
+  if ((st = encode_codes(mA, p.a, p.kp, p.M, int8::kBM)) != VEDA_OK ||
+      (st = encode_codes(mB, p.w, p.kp, p.N, int8::kBN)) != VEDA_OK)
+    return st;
+  int8::int8_gemm_kernel<T><<<grid_for(p.tiles, sms, 1), int8::kThreads, int8::kSmemBytes, s>>>(mA, mB, p);
+  return launched("int8_gemm_kernel");
+}
+}  // namespace
 
 extern "C" {
 
@@ -759,6 +829,222 @@ veda_status veda_rel_error(const void* o, const void* o_ref, float* sums, int32_
   heat::rel_error_kernel<<<static_cast<unsigned>(blocks), heat::kErrThreads, 0, s>>>(
       static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(o_ref), sums, rows, H);
   return launched("rel_error_kernel");
+}
+
+veda_status veda_rotary_table(const int32_t* positions, int32_t axes, int64_t rows, const double* inv_freq,
+                              const int32_t* axis, int32_t pairs, double amplitude, float* cos_sin,
+                              veda_stream_t stream) {
+  return guarded("veda_rotary_table", [&]() -> veda_status {
+    if (axes < 1 || axes > rotary::kMaxAxes || rows < 0 || pairs < 1 || pairs > rotary::kMaxPairs || !inv_freq || !axis)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_table: bad pointer or size");
+    if (rows > INT64_MAX / 4096) return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_table: too many rows");
+    rotary::TableArgs a{};
+    for (int32_t p = 0; p < pairs; ++p) {
+      if (axis[p] < 0 || axis[p] >= axes) return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_table: axis out of range");
+      if (!std::isfinite(inv_freq[p])) return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_table: inv_freq must be finite");
+      a.inv_freq[p] = inv_freq[p];
+      a.axis[p] = static_cast<uint8_t>(axis[p]);
+    }
+    if (!std::isfinite(amplitude)) return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_table: amplitude must be finite");
+    if (rows == 0) return VEDA_OK;
+    if (!positions || !cos_sin || !aligned(positions, 4) || !aligned(cos_sin, 16))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_table: missing or misaligned buffer");
+    int sms;
+    veda_status st = current_device(sms);
+    if (st != VEDA_OK) return st;
+    a.pos = positions; a.out = reinterpret_cast<float2*>(cos_sin);
+    a.rows = rows; a.pairs = pairs; a.amplitude = amplitude;
+    const int64_t blocks = (rows * pairs + rotary::kThreads - 1) / rotary::kThreads;
+    rotary::table_kernel<<<grid_for(blocks, sms, 8), rotary::kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return launched("table_kernel");
+  });
+}
+
+veda_status veda_rotary(const void* x, const int64_t* x_strides, void* y, const int64_t* y_strides, int32_t dtype,
+                        const float* cos_sin, int64_t table_rows, const int32_t* rows, int32_t rot_dim,
+                        int32_t interleaved, int32_t inverse, int32_t B, int32_t N, int32_t H, int32_t D,
+                        veda_stream_t stream) {
+  return guarded("veda_rotary", [&]() -> veda_status {
+    if (!x_strides || !y_strides || B < 0 || N < 0 || H < 0 || D <= 0 || !known_type(dtype) || table_rows < 0)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary: bad pointer, size or type");
+    if (D > 1024 || rot_dim < 2 || rot_dim > D || rot_dim > 2 * rotary::kMaxPairs || rot_dim % 2)
+      return fail(VEDA_ERR_UNSUPPORTED, "veda_rotary: rot_dim must be even, in [2, min(D, 512)], and D at most 1024");
+    if (!rows && table_rows != N && table_rows != static_cast<int64_t>(B) * N)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary: the table has neither N nor B * N rows");
+    if (B == 0 || N == 0 || H == 0) return VEDA_OK;
+    if (table_rows == 0) return fail(VEDA_ERR_INVALID_ARG, "veda_rotary: empty table");
+    const int64_t es = type_size(dtype);
+    if (!x || !y || !cos_sin || !aligned(x, es) || !aligned(y, es) || !aligned(cos_sin, 16) || !aligned(rows, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary: missing or misaligned buffer");
+    rotary::Args a{};
+    a.x = x; a.y = y;
+    bool same = x == y;
+    // 16-byte vectors: every row of x and y starts on such a boundary and the layout's parts are
+    // whole vectors; otherwise a lane takes one pair
+    const int32_t P = rot_dim / 2, E = static_cast<int32_t>(16 / es);
+    bool vec = aligned(x, 16) && aligned(y, 16) && D % E == 0 && (interleaved ? rot_dim % E == 0 : P % E == 0);
+    for (int i = 0; i < 3; ++i) {
+      a.xs[i] = x_strides[i];
+      a.ys[i] = y_strides[i];
+      vec = vec && x_strides[i] % E == 0 && y_strides[i] % E == 0;
+      same = same && x_strides[i] == y_strides[i];
+    }
+    a.cs = reinterpret_cast<const float2*>(cos_sin);
+    a.rows = rows; a.table_rows = table_rows;
+    a.batch_rows = table_rows == N ? 0 : N;
+    a.N = N; a.H = H; a.D = D; a.P = P;
+    a.sign = inverse ? -1.f : 1.f;
+    const int32_t VE = vec ? (interleaved ? E / 2 : E) : 1;
+    const int32_t W = vec ? (interleaved ? E : 2 * E) : 2;
+    a.rot_items = P / VE;
+    // in place, the channels behind the rotated ones stay where they are
+    a.items = a.rot_items + (same && !rows ? 0 : (D - rot_dim + W - 1) / W);
+    a.width_log2 = 0;
+    while (a.width_log2 < 5 && (1 << a.width_log2) < a.items) ++a.width_log2;
+    int sms;
+    veda_status st = current_device(sms);
+    if (st != VEDA_OK) return st;
+    // heads per warp: all of a token's, so that its cos / sin are loaded once, unless that leaves
+    // SMs without work; never fewer than one pass of the warp
+    const int64_t tokens = static_cast<int64_t>(B) * N;
+    const int32_t side = 32 >> a.width_log2;
+    a.hg = H;
+    while (a.hg > side && tokens * ((H + a.hg - 1) / a.hg) < static_cast<int64_t>(sms) * 2 * rotary::kWarps)
+      a.hg = std::max(side, (a.hg + 1) / 2);
+    a.groups = (H + a.hg - 1) / a.hg;
+    a.units = tokens * a.groups;
+    const int64_t blocks = (a.units + rotary::kWarps - 1) / rotary::kWarps;
+    if (blocks > INT32_MAX) return fail(VEDA_ERR_UNSUPPORTED, "veda_rotary: too many tokens");
+    using BF = __nv_bfloat16;
+    typedef void (*Kernel)(const rotary::Args);
+    static const Kernel kernels[3][2][2] = {   // [type][half layout][vectors]
+        {{rotary::rotary_kernel<BF, false, false>, rotary::rotary_kernel<BF, false, true>},
+         {rotary::rotary_kernel<BF, true, false>, rotary::rotary_kernel<BF, true, true>}},
+        {{rotary::rotary_kernel<__half, false, false>, rotary::rotary_kernel<__half, false, true>},
+         {rotary::rotary_kernel<__half, true, false>, rotary::rotary_kernel<__half, true, true>}},
+        {{rotary::rotary_kernel<float, false, false>, rotary::rotary_kernel<float, false, true>},
+         {rotary::rotary_kernel<float, true, false>, rotary::rotary_kernel<float, true, true>}}};
+    kernels[dtype][interleaved ? 0 : 1][vec ? 1 : 0]<<<static_cast<unsigned>(blocks), rotary::kThreads, 0,
+                                                       reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return launched("rotary_kernel");
+  });
+}
+
+veda_status veda_rotary_permute_pool(const void* x, void* x_tiled, const float* cos_sin, int64_t table_rows,
+                                     int32_t rot_dim, int32_t interleaved, const int32_t* tile_map,
+                                     const int32_t* tile_valid, float* pooled, int32_t B, int32_t N, int32_t H,
+                                     int32_t D, int32_t Npad, veda_stream_t stream) {
+  return guarded("veda_rotary_permute_pool", [&]() -> veda_status {
+    if (!x || !x_tiled || !tile_map || !tile_valid || !pooled || B <= 0 || N <= 0 || H <= 0 || Npad <= 0 || Npad % 128)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_permute_pool: bad pointer or size");
+    veda_status st = check_tile_rotation("veda_rotary_permute_pool", cos_sin, table_rows, rot_dim, B, N, D);
+    if (st != VEDA_OK) return st;
+    if (!aligned(x, 16) || !aligned(x_tiled, 16) || !aligned(pooled, 16) || !aligned(tile_map, 4) || !aligned(tile_valid, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_permute_pool: misaligned buffer");
+    int sms;
+    if ((st = current_device(sms)) != VEDA_OK) return st;
+    rotary::TileArgs p{};
+    p.g = {static_cast<const uint8_t*>(x), static_cast<uint8_t*>(x_tiled), tile_map, B, N, H, Npad, Npad / 128,
+           static_cast<int64_t>(B) * H * (Npad / 128)};
+    p.valid = tile_valid; p.pooled = pooled;
+    p.cs = reinterpret_cast<const float2*>(cos_sin);
+    p.batch_rows = table_rows == N ? 0 : N;
+    p.P = rot_dim / 2; p.sign = 1.f;
+    const int64_t ctas = (p.g.units + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
+    auto* k = interleaved ? rotary::rotary_permute_pool_kernel<false> : rotary::rotary_permute_pool_kernel<true>;
+    const DeviceInfo& d = device_info();
+    k<<<grid_for(ctas, sms, interleaved ? d.per_sm_rotpool[0] : d.per_sm_rotpool[1]), kPoolThreads, 0,
+        reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launched("rotary_permute_pool_kernel");
+  });
+}
+
+veda_status veda_rotary_unpermute(const void* x_tiled, void* x, const float* cos_sin, int64_t table_rows,
+                                  int32_t rot_dim, int32_t interleaved, int32_t inverse, const int32_t* tile_map,
+                                  int32_t B, int32_t N, int32_t H, int32_t D, int32_t Npad, veda_stream_t stream) {
+  return guarded("veda_rotary_unpermute", [&]() -> veda_status {
+    if (!x || !x_tiled || !tile_map || B <= 0 || N <= 0 || H <= 0 || Npad <= 0 || Npad % 128)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_unpermute: bad pointer or size");
+    veda_status st = check_tile_rotation("veda_rotary_unpermute", cos_sin, table_rows, rot_dim, B, N, D);
+    if (st != VEDA_OK) return st;
+    if (!aligned(x, 16) || !aligned(x_tiled, 16) || !aligned(tile_map, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_rotary_unpermute: misaligned buffer");
+    int sms;
+    if ((st = current_device(sms)) != VEDA_OK) return st;
+    rotary::TileArgs p{};
+    p.g = {static_cast<const uint8_t*>(x_tiled), static_cast<uint8_t*>(x), tile_map, B, N, H, Npad, Npad / 128,
+           static_cast<int64_t>(B) * H * (Npad / 128)};
+    p.cs = reinterpret_cast<const float2*>(cos_sin);
+    p.batch_rows = table_rows == N ? 0 : N;
+    p.P = rot_dim / 2; p.sign = inverse ? -1.f : 1.f;
+    auto* k = interleaved ? rotary::rotary_unpermute_kernel<false> : rotary::rotary_unpermute_kernel<true>;
+    const DeviceInfo& d = device_info();
+    k<<<grid_for(p.g.units, sms, interleaved ? d.per_sm_rotback[0] : d.per_sm_rotback[1]), kCopyThreads, 0,
+        reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launched("rotary_unpermute_kernel");
+  });
+}
+
+veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t dtype, void* codes, float* scale, int64_t rows,
+                               int32_t K, veda_stream_t stream) {
+  return guarded("veda_quantize_int8", [&]() -> veda_status {
+    if (rows < 0 || rows > INT32_MAX || K <= 0 || K > INT32_MAX - 16 || !known_type(dtype))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_quantize_int8: bad size or type");
+    if (rows == 0) return VEDA_OK;
+    const int64_t es = type_size(dtype);
+    if (!x || !codes || !scale || !aligned(x, es) || !aligned(codes, 16) || !aligned(scale, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_quantize_int8: missing or misaligned buffer");
+    int sms;
+    veda_status st = current_device(sms);
+    if (st != VEDA_OK) return st;
+    int8::QuantArgs a{x, x_stride, static_cast<int8_t*>(codes), scale, rows, K, (K + 15) / 16 * 16,
+                      aligned(x, 16) && x_stride * es % 16 == 0 ? 1 : 0};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (a.kp <= int8::kQuantWarpK) {
+      const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+      if (dtype == VEDA_BF16) int8::quant_warp_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+      else if (dtype == VEDA_FP16) int8::quant_warp_kernel<__half><<<grid, 256, 0, s>>>(a);
+      else int8::quant_warp_kernel<float><<<grid, 256, 0, s>>>(a);
+    } else {
+      const unsigned grid = static_cast<unsigned>(rows);
+      if (dtype == VEDA_BF16) int8::quant_row_kernel<__nv_bfloat16><<<grid, int8::kQuantThreads, 0, s>>>(a);
+      else if (dtype == VEDA_FP16) int8::quant_row_kernel<__half><<<grid, int8::kQuantThreads, 0, s>>>(a);
+      else int8::quant_row_kernel<float><<<grid, int8::kQuantThreads, 0, s>>>(a);
+    }
+    return launched("quantize_int8");
+  });
+}
+
+veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w, const float* w_scale,
+                             const float* bias, void* y, int64_t y_stride, int32_t dtype, int32_t M, int32_t N,
+                             int32_t K, veda_stream_t stream) {
+  return guarded("veda_int8_matmul", [&]() -> veda_status {
+    if (M < 0 || N < 0 || K <= 0 || !known_type(dtype) || y_stride < 0)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_matmul: bad size or type");
+    if (K > 131071) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_matmul: K above 131071 overflows the integer sum");
+    if (M == 0 || N == 0) return VEDA_OK;
+    const int64_t es = type_size(dtype);
+    if (!a || !a_scale || !w || !w_scale || !y || !aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) ||
+        !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(y, es))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_matmul: missing or misaligned buffer");
+    if (M > 1 && y_stride < N) return fail(VEDA_ERR_INVALID_ARG, "veda_int8_matmul: rows of y overlap");
+    int sms;
+    veda_status st = current_device(sms);
+    if (st != VEDA_OK) return st;
+    int8::MatArgs p{};
+    p.a = static_cast<const int8_t*>(a); p.w = static_cast<const int8_t*>(w);
+    p.sa = a_scale; p.sw = w_scale; p.bias = bias;
+    p.out = y; p.ldo = y_stride;
+    p.M = M; p.N = N; p.kp = (K + 15) / 16 * 16;
+    p.chunks = (p.kp + 127) / 128;
+    p.tiles_m = (M - 1) / int8::kBM + 1; p.tiles_n = (N - 1) / int8::kBN + 1;
+    p.tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    p.out_vec = aligned(y, 16) && y_stride * es % 16 == 0;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == VEDA_BF16) return launch_int8<__nv_bfloat16>(p, sms, s);
+    if (dtype == VEDA_FP16) return launch_int8<__half>(p, sms, s);
+    return launch_int8<float>(p, sms, s);
+  });
 }
 
 // Self-test of the bounded waits: one thread waits on an mbarrier that nothing arrives

@@ -1,0 +1,265 @@
+// veda_norm.cu -- the C ABI of the norms around a block (include/veda.h): argument checks and
+// launches. Kernels in k_norm.cuh.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "k_norm.cuh"
+#include "veda_host.h"
+
+namespace veda {
+namespace {
+
+using norm::Args;
+
+veda_status fail(veda_status st, const std::string& msg) {
+  set_last_error(msg);
+  return st;
+}
+veda_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(VEDA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+bool known(int32_t dtype) { return dtype >= VEDA_BF16 && dtype <= VEDA_FP32; }
+int64_t size_of(int32_t dtype) { return dtype == VEDA_FP32 ? 4 : 2; }
+bool on(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a) == 0; }
+
+// Rows of this tensor start on 16-byte boundaries.
+bool vec_rows(const void* p, int64_t sb, int64_t sn, int32_t dtype) {
+  return on(p, 16) && sb * size_of(dtype) % 16 == 0 && sn * size_of(dtype) % 16 == 0;
+}
+
+// Rows in the ring: enough bytes in flight for the HBM's latency (Little's law asks for about
+// 45 KB an SM), fewer where a CTA's ring would not fit its share of shared memory.
+constexpr int kFwdStages = 4, kBwdStages = 3;
+constexpr int kMaxRing = 224 * 1024;
+
+struct Shape {
+  int nv;          // vectors per thread
+  bool warp;       // a row per warp
+  int threads;     // per CTA
+};
+Shape shape_of(int32_t C) {
+  const int vecs = (C + norm::kVec - 1) / norm::kVec;
+  if (C <= 256) return {1, true, 32 * norm::kWarpsPerCta};
+  if (C <= 512) return {2, true, 32 * norm::kWarpsPerCta};
+  if (C <= norm::kWarpCols) return {4, true, 32 * norm::kWarpsPerCta};
+  return {2, false, ((vecs + 1) / 2 + 31) / 32 * 32};     // at most kMaxThreads
+}
+
+typedef void (*Kernel)(const Args);
+
+// The kernels of one shape and type pair; null for a pair that is not built.
+template <int NV, bool W>
+Kernel pick_types(bool bwd, int32_t ti, int32_t to) {
+  using B = __nv_bfloat16;
+  using H = __half;
+#define VEDA_PAIR(TI, TO) (bwd ? norm::norm_bwd_kernel<TI, TO, NV, W> : norm::norm_fwd_kernel<TI, TO, NV, W>)
+  if (ti == VEDA_BF16 && to == VEDA_BF16) return VEDA_PAIR(B, B);
+  if (ti == VEDA_FP16 && to == VEDA_FP16) return VEDA_PAIR(H, H);
+  if (ti == VEDA_FP32 && to == VEDA_FP32) return VEDA_PAIR(float, float);
+  if (ti == VEDA_FP32 && to == VEDA_BF16) return VEDA_PAIR(float, B);
+  if (ti == VEDA_BF16 && to == VEDA_FP32) return VEDA_PAIR(B, float);
+#undef VEDA_PAIR
+  return nullptr;
+}
+Kernel pick(const Shape& s, bool bwd, int32_t ti, int32_t to) {
+  if (s.warp) {
+    if (s.nv == 1) return pick_types<1, true>(bwd, ti, to);
+    if (s.nv == 2) return pick_types<2, true>(bwd, ti, to);
+    return pick_types<4, true>(bwd, ti, to);
+  }
+  return pick_types<2, false>(bwd, ti, to);
+}
+
+// Ring bytes of a CTA: every row a group has in flight, 16-byte units.
+int ring_bytes(const Shape& s, bool bwd, int32_t ti, int32_t to, bool res, int32_t& stages) {
+  const int ui = ti == VEDA_FP32 ? 2 : 1, uo = to == VEDA_FP32 ? 2 : 1;
+  const int units = bwd ? ui + uo + (res ? ui : 0) : ui + (res ? uo : 0);
+  const int row = s.nv * units * s.threads * 16;            // <= 96 KB (fp32, 8,192 channels)
+  stages = bwd ? kBwdStages : kFwdStages;
+  while (stages > 2 && stages * row > kMaxRing) --stages;
+  return stages * row;
+}
+
+// Slices per sequence: together the CTAs that can run at once (so a CTA keeps its channels'
+// parameters for as many rows as possible), no more than there are rows.
+constexpr int kMaxPerSmFwd = 8, kMaxPerSmBwd = 4, kMaxSms = 160;
+veda_status slices_for(Kernel k, const Shape& s, int bytes, int sms, int cap, int32_t B, int32_t N, int32_t& slices) {
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(k),
+                                                                      s.threads, static_cast<size_t>(bytes));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  per_sm = std::max(1, std::min(per_sm, cap));
+  const int64_t want = (static_cast<int64_t>(std::min(sms, kMaxSms)) * per_sm + B - 1) / B;
+  const int64_t rows = s.warp ? (N + norm::kWarpsPerCta - 1) / norm::kWarpsPerCta : N;
+  slices = static_cast<int32_t>(std::max<int64_t>(1, std::min(want, rows)));
+  return VEDA_OK;
+}
+
+// Rings over the default limit (48 KB with the static part) need an opt-in; always the same one,
+// so that calls from two threads cannot take it from one another.
+veda_status allow_smem(Kernel k, int bytes) {
+  if (bytes <= 32 * 1024) return VEDA_OK;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+  return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "cudaFuncSetAttribute");
+}
+
+veda_status check_common(const char* call, int32_t x_dtype, int32_t y_dtype, const veda_norm_params* q, int32_t B,
+                         int32_t N, int32_t C, int32_t kind, float eps) {
+  const std::string c(call);
+  if (B < 0 || N < 0 || N > INT32_MAX - 1024 || C <= 0) return fail(VEDA_ERR_INVALID_ARG, c + ": bad size");
+  if (!known(x_dtype) || !known(y_dtype) || !q || !known(q->weight_dtype) || !known(q->mod_dtype))
+    return fail(VEDA_ERR_INVALID_ARG, c + ": unknown type");
+  if (kind < VEDA_NORM_LAYER || kind > VEDA_NORM_NONE) return fail(VEDA_ERR_INVALID_ARG, c + ": unknown kind of norm");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(VEDA_ERR_INVALID_ARG, c + ": eps must be finite and >= 0");
+  if (C > norm::kMaxCols) return fail(VEDA_ERR_UNSUPPORTED, c + ": more than 8192 channels");
+  if (!pick({1, true, 0}, false, x_dtype, y_dtype))
+    return fail(VEDA_ERR_UNSUPPORTED, c + ": input and output types must be equal, or bf16 and fp32");
+  const int64_t ws = size_of(q->weight_dtype), ms = size_of(q->mod_dtype);
+  if (!on(q->weight, ws) || !on(q->bias, ws) || !on(q->gain, ms) || !on(q->shift, ms))
+    return fail(VEDA_ERR_INVALID_ARG, c + ": misaligned parameter");
+  return VEDA_OK;
+}
+
+void set_params(Args& a, const veda_norm_params* q) {
+  a.w = {q->weight, 0, q->weight_dtype};
+  a.b = {q->bias, 0, q->weight_dtype};
+  a.g = {q->gain, q->gain_stride, q->mod_dtype};
+  a.t = {q->shift, q->shift_stride, q->mod_dtype};
+  a.gain_off = q->gain_offset;
+}
+
+}  // namespace
+}  // namespace veda
+
+using namespace veda;
+
+extern "C" {
+
+veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const veda_rows* y,
+                          const veda_norm_params* params, float residual_scale, float* mean, float* rstd, int32_t B,
+                          int32_t N, int32_t C, int32_t kind, float eps, veda_stream_t stream) {
+  return guarded("veda_norm_fwd", [&]() -> veda_status {
+    const char* call = "veda_norm_fwd";
+    if (!x || !y) return fail(VEDA_ERR_INVALID_ARG, "veda_norm_fwd: no input or output");
+    veda_status st = check_common(call, x->dtype, y->dtype, params, B, N, C, kind, eps);
+    if (st != VEDA_OK) return st;
+    if (residual && residual->dtype != y->dtype)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_fwd: the residual has the output's type");
+    if ((mean && !rstd)) return fail(VEDA_ERR_INVALID_ARG, "veda_norm_fwd: mean without rstd");
+    if (B == 0 || N == 0) return VEDA_OK;
+    if (!x->data || !y->data || (residual && !residual->data) || !on(x->data, size_of(x->dtype)) ||
+        !on(y->data, size_of(y->dtype)) || (residual && !on(residual->data, size_of(y->dtype))) || !on(mean, 4) ||
+        !on(rstd, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_fwd: bad pointer");
+    int sms;
+    if ((st = host_device(sms)) != VEDA_OK) return st;
+    Args a{};
+    a.x = x->data; a.xb = x->batch_stride; a.xn = x->row_stride;
+    a.y = y->data; a.yb = y->batch_stride; a.yn = y->row_stride;
+    if (residual) { a.res = residual->data; a.rb = residual->batch_stride; a.rn = residual->row_stride; }
+    set_params(a, params);
+    a.res_scale = residual_scale; a.eps = eps; a.inv_c = 1.0f / static_cast<float>(C);
+    a.mean = mean; a.rstd = rstd;
+    a.B = B; a.N = N; a.C = C; a.kind = kind;
+    a.vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.y, a.yb, a.yn, y->dtype) &&
+            (!residual || vec_rows(a.res, a.rb, a.rn, y->dtype));
+    const Shape s = shape_of(C);
+    const int bytes = ring_bytes(s, false, x->dtype, y->dtype, residual != nullptr, a.stages);
+    const Kernel k = pick(s, false, x->dtype, y->dtype);
+    if ((st = allow_smem(k, bytes)) != VEDA_OK) return st;
+    if ((st = slices_for(k, s, bytes, sms, kMaxPerSmFwd, B, N, a.slices)) != VEDA_OK) return st;
+    k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "norm_fwd_kernel");
+  });
+}
+
+size_t veda_norm_bwd_workspace_bytes(int32_t B, int32_t N, int32_t C) {
+  if (B <= 0 || N <= 0 || C <= 0 || C > norm::kMaxCols) return 0;
+  // partial sums of every slice (slices_for: fewer than kMaxSms * kMaxPerSmBwd + B in all, and at
+  // most one a row), then one row pair per sequence
+  const int64_t slices = std::min<int64_t>(static_cast<int64_t>(B) * N, kMaxSms * kMaxPerSmBwd + B);
+  return static_cast<size_t>((slices + B) * 2 * C) * sizeof(float);
+}
+
+veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* mean, const float* rstd,
+                          const veda_rows* residual_grad, const veda_rows* dx, const veda_norm_params* params,
+                          float residual_scale, float* dgain, float* dshift, float* dweight, float* dbias,
+                          void* workspace, size_t workspace_bytes, int32_t B, int32_t N, int32_t C, int32_t kind,
+                          veda_stream_t stream) {
+  return guarded("veda_norm_bwd", [&]() -> veda_status {
+    const char* call = "veda_norm_bwd";
+    if (!dy || !x || !dx) return fail(VEDA_ERR_INVALID_ARG, "veda_norm_bwd: no input or output");
+    veda_status st = check_common(call, x->dtype, dy->dtype, params, B, N, C, kind, 0.f);
+    if (st != VEDA_OK) return st;
+    if (dx->dtype != x->dtype || (residual_grad && residual_grad->dtype != x->dtype))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_bwd: dx and the gradient around the block have x's type");
+    const cudaStream_t s0 = reinterpret_cast<cudaStream_t>(stream);
+    if (!on(dgain, 4) || !on(dshift, 4) || !on(dweight, 4) || !on(dbias, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_bwd: misaligned gradient");
+    int sms;
+    if (B == 0 || N == 0) {           // no token: the parameters' gradients are zero
+      if ((st = host_device(sms)) != VEDA_OK) return st;
+      cudaError_t e = cudaSuccess;
+      const size_t row = static_cast<size_t>(C) * sizeof(float);
+      if (dgain && B && e == cudaSuccess) e = cudaMemsetAsync(dgain, 0, row * B, s0);
+      if (dshift && B && e == cudaSuccess) e = cudaMemsetAsync(dshift, 0, row * B, s0);
+      if (dweight && e == cudaSuccess) e = cudaMemsetAsync(dweight, 0, row, s0);
+      if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, row, s0);
+      return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "cudaMemsetAsync");
+    }
+    if (!dy->data || !x->data || !dx->data || (residual_grad && !residual_grad->data) ||
+        !on(dy->data, size_of(dy->dtype)) || !on(x->data, size_of(x->dtype)) || !on(dx->data, size_of(x->dtype)) ||
+        (residual_grad && !on(residual_grad->data, size_of(x->dtype))))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_bwd: bad pointer");
+    if ((kind != VEDA_NORM_NONE && !rstd) || (kind == VEDA_NORM_LAYER && !mean) || !on(mean, 4) || !on(rstd, 4))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_bwd: the forward's statistics are missing");
+    if (!workspace || !on(workspace, 16) || workspace_bytes < veda_norm_bwd_workspace_bytes(B, N, C))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_norm_bwd: workspace too small or misaligned");
+    if (B > 65535) return fail(VEDA_ERR_UNSUPPORTED, "veda_norm_bwd: more than 65535 sequences");
+    if ((st = host_device(sms)) != VEDA_OK) return st;
+    Args a{};
+    a.x = x->data; a.xb = x->batch_stride; a.xn = x->row_stride;
+    a.dy = dy->data; a.db = dy->batch_stride; a.dn = dy->row_stride;
+    a.y = dx->data; a.yb = dx->batch_stride; a.yn = dx->row_stride;
+    if (residual_grad) { a.res = residual_grad->data; a.rb = residual_grad->batch_stride; a.rn = residual_grad->row_stride; }
+    set_params(a, params);
+    a.res_scale = residual_scale; a.inv_c = 1.0f / static_cast<float>(C);
+    a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+    a.B = B; a.N = N; a.C = C; a.kind = kind;
+    a.vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.dy, a.db, a.dn, dy->dtype) &&
+            vec_rows(a.y, a.yb, a.yn, x->dtype) && (!a.res || vec_rows(a.res, a.rb, a.rn, x->dtype));
+    const Shape s = shape_of(C);
+    const int bytes = ring_bytes(s, true, x->dtype, dy->dtype, a.res != nullptr, a.stages);
+    a.part = static_cast<float*>(workspace);
+    const Kernel k = pick(s, true, x->dtype, dy->dtype);
+    if ((st = allow_smem(k, bytes)) != VEDA_OK) return st;
+    if ((st = slices_for(k, s, bytes, sms, kMaxPerSmBwd, B, N, a.slices)) != VEDA_OK) return st;
+    k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, s0>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "norm_bwd_kernel");
+    if (!dgain && !dshift && !dweight && !dbias) return VEDA_OK;
+    norm::GradArgs g{};
+    g.part = a.part;
+    g.w = a.w; g.b = a.b; g.g = a.g;
+    g.gain_off = a.gain_off;
+    g.dgain = dgain; g.dshift = dshift;
+    g.B = B; g.C = C; g.slices = a.slices;
+    g.gp = dweight || dbias ? a.part + static_cast<int64_t>(B) * a.slices * 2 * C : nullptr;
+    norm::norm_grad_kernel<<<dim3((C + 31) / 32, B), 32 * norm::kGradRows, 0, s0>>>(g);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "norm_grad_kernel");
+    if (g.gp) {
+      norm::norm_weight_grad_kernel<<<(C + 255) / 256, 256, 0, s0>>>(g.gp, dweight, dbias, B, C);
+      if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "norm_weight_grad_kernel");
+    }
+    return VEDA_OK;
+  });
+}
+
+}  // extern "C"

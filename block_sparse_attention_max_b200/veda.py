@@ -31,6 +31,9 @@ EXPORTED = (
     "veda_block_sparse_attn_bwd", "veda_block_heat", "veda_mask_quality", "veda_rel_error",
     "veda_tile_plan_vote",
     "veda_quantize_fp8", "veda_block_sparse_attn_fwd_fp8",
+    "veda_rotary_table", "veda_rotary", "veda_rotary_permute_pool", "veda_rotary_unpermute",
+    "veda_norm_fwd", "veda_norm_bwd_workspace_bytes", "veda_norm_bwd",
+    "veda_quantize_int8", "veda_int8_matmul",
     "veda_check_device_status", "veda_selftest_wait_timeout",
 )
 
@@ -53,9 +56,23 @@ class Geometry(ctypes.Structure):
                 ("order_stride", ctypes.c_int32)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class _NormParams(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("gain", ctypes.c_void_p),
+                ("shift", ctypes.c_void_p), ("gain_stride", ctypes.c_int64), ("shift_stride", ctypes.c_int64),
+                ("weight_dtype", ctypes.c_int32), ("mod_dtype", ctypes.c_int32), ("gain_offset", ctypes.c_float)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
+_L = ctypes.c_int64
+_D = ctypes.c_double
+_Z = ctypes.c_size_t
 _I = ctypes.c_int32
 _F = ctypes.c_float
 _SIG = {
@@ -85,6 +102,15 @@ _SIG = {
     "veda_block_heat": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _F, _P, _I, _I, _I, _I, _P]),
     "veda_mask_quality": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P, _P,
                                _I, _I, _I, _P]),
+    "veda_rotary_table": (_I, [_P, _I, _L, _P, _P, _I, _D, _P, _P]),
+    "veda_rotary": (_I, [_P, _P, _P, _P, _I, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "veda_rotary_permute_pool": (_I, [_P, _P, _P, _L, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "veda_rotary_unpermute": (_I, [_P, _P, _P, _L, _I, _I, _I, _P, _I, _I, _I, _I, _I, _P]),
+    "veda_norm_fwd": (_I, [_P, _P, _P, _P, _F, _P, _P, _I, _I, _I, _I, _F, _P]),
+    "veda_norm_bwd_workspace_bytes": (_Z, [_I, _I, _I]),
+    "veda_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _Z, _I, _I, _I, _I, _P]),
+    "veda_quantize_int8": (_I, [_P, _L, _I, _P, _P, _L, _I, _P]),
+    "veda_int8_matmul": (_I, [_P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _P]),
     "veda_check_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "veda_selftest_wait_timeout": (_I, [ctypes.c_uint32, _P]),
 }
@@ -590,6 +616,506 @@ def unpermute(o_t: torch.Tensor, maps: DeviceMaps, N: int, out: Optional[torch.T
     return out
 
 
+# ---------------------------------------------------------------------------------------
+# the block around the attention: rotary positions, norms, 8-bit integer projections
+# ---------------------------------------------------------------------------------------
+
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_KIND = {"layer": 0, "rms": 1, "none": 2}
+
+
+def _need_strided(t: torch.Tensor, name: str, ndim: int, dtype: Optional[torch.dtype] = None,
+                  shape: Optional[Sequence[int]] = None, written: bool = False) -> None:
+    """Checks of a tensor whose leading dimensions may have any stride: type, shape, device,
+    contiguous channels, and, where the library writes it, no two elements in one place."""
+    if dtype is None and t.dtype not in _DTYPE:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got shape {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(int(x) for x in shape):
+        raise ValueError(f"{name}: expected shape {tuple(int(x) for x in shape)}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if written and t.numel() > 0 and not t.is_contiguous():
+        extent = 1
+        for st, n in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+            if st < extent:
+                raise ValueError(f"{name}: elements overlap in memory")
+            extent = st * (n - 1) + extent
+
+
+def _separate(out: torch.Tensor, t: Optional[torch.Tensor], name: str, same_ok: bool) -> None:
+    """out may be t itself (where same_ok), else they must not share memory."""
+    if t is None or out.numel() == 0 or t.numel() == 0:
+        return
+    if out.data_ptr() == t.data_ptr() and out.stride() == t.stride() and out.shape == t.shape and out.dtype == t.dtype:
+        if same_ok:
+            return
+        raise ValueError(f"out must not be {name}")
+    span = lambda x: (x.data_ptr(), x.data_ptr() + x.element_size() * (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride()))))
+    a, b = span(out), span(t)
+    if a[0] < b[1] and b[0] < a[1]:
+        raise ValueError(f"out overlaps {name} in memory")
+
+
+def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """A buffer for work on `stream` (None: the current one): taken from that stream's memory,
+    and kept from reuse until what the current stream does with it later has run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+@dataclasses.dataclass
+class RotaryFrequencies:
+    """Pairs of a rotated head: inverse frequency (fp64) and position axis of each, and the
+    amplitude of the turned vectors."""
+    inv_freq: np.ndarray
+    axis: np.ndarray
+    amplitude: float = 1.0
+
+
+def rotary_frequencies(dims, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0) -> RotaryFrequencies:
+    """Frequencies theta^(-2 i / d), i < d / 2, for the d channels of each position axis (``dims``:
+    an even count per axis, e.g. (44, 42, 42) for time, height and width; an int for one axis).
+
+    Scalings for contexts ``factor`` times as long as trained on: ``linear`` divides every
+    frequency by the factor (position interpolation); ``ntk`` raises theta to
+    theta * factor^(d / (d - 2)), which keeps the fastest pair and slows the slowest by the factor;
+    ``yarn`` (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models")
+    keeps the pairs that turn more than beta_fast times within original_length, divides those that
+    turn less than beta_slow times by the factor, goes linearly in the pair index between, and
+    scales the turned vectors by 0.1 ln(factor) + 1.
+    """
+    dims = [int(dims)] if isinstance(dims, (int, np.integer)) else [int(d) for d in dims]
+    if not dims or any(d < 0 or d % 2 for d in dims) or sum(dims) == 0:
+        raise ValueError("dims: expected even channel counts")
+    if not (theta > 1.0) or not (factor >= 1.0):
+        raise ValueError("theta must be above 1 and factor at least 1")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError("scaling must be none, linear, ntk or yarn")
+    if scaling == "yarn" and (original_length <= 0 or not beta_fast > beta_slow > 0):
+        raise ValueError("yarn needs original_length > 0 and beta_fast > beta_slow > 0")
+    inv, axis, amplitude = [], [], 1.0
+    for a, d in enumerate(dims):
+        if d == 0:
+            continue
+        i = np.arange(d // 2, dtype=np.float64)
+        base = float(theta)
+        if scaling == "ntk":
+            if d <= 2:
+                raise ValueError("ntk scaling needs more than 2 channels per axis")
+            base *= float(factor) ** (d / (d - 2))
+        f = base ** (-2.0 * i / d)
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            pair = lambda turns: d * np.log(original_length / (2 * np.pi * turns)) / (2 * np.log(theta))
+            low, high = max(np.floor(pair(beta_fast)), 0.0), min(np.ceil(pair(beta_slow)), d / 2 - 1.0)
+            ramp = np.clip((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+            f = f * (1.0 - ramp) + f / factor * ramp
+            amplitude = 0.1 * float(np.log(factor)) + 1.0
+        inv.append(f)
+        axis.append(np.full(d // 2, a, np.int32))
+    return RotaryFrequencies(np.concatenate(inv), np.concatenate(axis), amplitude)
+
+
+def rotary_positions(grid, n_tail: int = 0) -> np.ndarray:
+    """[3, N] int32 (t, h, w) of a geometry's raster tokens; appended 1D token j has the position
+    max(T, Hg, Wg) + j on all three axes (behind every video position)."""
+    T, Hg, Wg = (int(x) for x in grid)
+    t, h, w = np.meshgrid(np.arange(T), np.arange(Hg), np.arange(Wg), indexing="ij")
+    tail = np.tile(max(T, Hg, Wg) + np.arange(int(n_tail)), (3, 1))
+    return np.concatenate([np.stack([t.ravel(), h.ravel(), w.ravel()]), tail], 1).astype(np.int32)
+
+
+@dataclasses.dataclass
+class RotaryTable:
+    """cos / sin of every (row, pair): fp32 [rows, P, 2]; rot_dim = 2 P channels are turned, in
+    interleaved pairs (2p, 2p + 1) or, in the half layout, (p, p + P)."""
+    cos_sin: torch.Tensor
+    interleaved: bool
+
+    @property
+    def rows(self) -> int:
+        return self.cos_sin.shape[0]
+
+    @property
+    def rot_dim(self) -> int:
+        return 2 * self.cos_sin.shape[1]
+
+    def _check(self) -> None:
+        if self.cos_sin.dim() != 3 or self.cos_sin.shape[2] != 2:
+            raise ValueError("cos_sin: expected shape [rows, P, 2]")
+        _need(self.cos_sin, torch.float32, "cos_sin")
+
+
+def rotary_table(positions: torch.Tensor, inv_freq: np.ndarray, axis: Optional[np.ndarray] = None,
+                 amplitude: float = 1.0, interleaved: bool = True, out: Optional[torch.Tensor] = None,
+                 stream=None) -> RotaryTable:
+    """veda_rotary_table: positions int32 [rows] or [axes, rows] on the device; inv_freq / axis
+    [P] on the host (see ``rotary_frequencies``; axis defaults to 0)."""
+    if positions.dim() == 1:
+        positions = positions.unsqueeze(0)
+    if positions.dim() != 2:
+        raise ValueError("positions: expected shape [rows] or [axes, rows]")
+    _need(positions, torch.int32, "positions")
+    inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    ax = np.zeros(inv.shape, np.int32) if axis is None else np.ascontiguousarray(axis, dtype=np.int32)
+    if inv.ndim != 1 or ax.shape != inv.shape:
+        raise ValueError("inv_freq / axis: expected equal shapes [P]")
+    axes, rows = positions.shape
+    if out is None:
+        out = _new((rows, len(inv), 2), torch.float32, positions.device, stream)
+    _need(out, torch.float32, "out", shape=(rows, len(inv), 2))
+    _check("veda_rotary_table", lib().veda_rotary_table(
+        _ptr(positions), axes, rows, inv.ctypes.data, ax.ctypes.data, len(inv), float(amplitude), _ptr(out),
+        _stream(stream)))
+    return RotaryTable(out, bool(interleaved))
+
+
+def rotary(x: torch.Tensor, table: RotaryTable, rows: Optional[torch.Tensor] = None, inverse: bool = False,
+           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """veda_rotary: x [B, N, H, D] (bf16, fp16 or fp32; any strides, channels contiguous) turned by
+    the table's row of each token -- row n, row b N + n (a table of B N rows), or rows[b, n]
+    (int32). ``inverse`` is the transpose, which the gradient takes. ``out`` may be x."""
+    _need_strided(x, "x", 4)
+    B, N, H, D = x.shape
+    table._check()
+    if out is None:
+        out = _new((B, N, H, D), x.dtype, x.device, stream)
+    _need_strided(out, "out", 4, x.dtype, x.shape, written=True)
+    _separate(out, x, "x", True)
+    _separate(out, table.cos_sin, "the table", False)
+    if rows is not None:
+        _need(rows, torch.int32, "rows", shape=(B, N))
+    xs = (ctypes.c_int64 * 3)(*x.stride()[:3])
+    ys = (ctypes.c_int64 * 3)(*out.stride()[:3])
+    _check("veda_rotary", lib().veda_rotary(
+        _ptr(x), ctypes.addressof(xs), _ptr(out), ctypes.addressof(ys), _DTYPE[x.dtype], _ptr(table.cos_sin),
+        table.rows, _ptr(rows), table.rot_dim, int(table.interleaved), int(bool(inverse)), B, N, H, D,
+        _stream(stream)))
+    return out
+
+
+def rotary_permute_pool(x: torch.Tensor, table: RotaryTable, maps: DeviceMaps, out: Optional[torch.Tensor] = None,
+                        pooled: Optional[torch.Tensor] = None, stream=None):
+    """veda_rotary_permute_pool: ``permute_pool`` with the rotation of ``rotary`` on the way (the
+    pooled features are those of the turned values before they are rounded to bf16)."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 4:
+        raise ValueError("x: expected shape [B, N, H, 128]")
+    B, N, H, D = x.shape
+    _need_maps(maps, H, maps.Npad)
+    table._check()
+    if out is None:
+        out = _new((B, H, maps.Npad, D), torch.bfloat16, x.device, stream)
+    if pooled is None:
+        pooled = _new((B, H, maps.Npad // 128, 3, D), torch.float32, x.device, stream)
+    _need(out, torch.bfloat16, "out", shape=(B, H, maps.Npad, D))
+    _need(pooled, torch.float32, "pooled", shape=(B, H, maps.Npad // 128, 3, D))
+    _separate(out, x, "x", False)
+    _check("veda_rotary_permute_pool", lib().veda_rotary_permute_pool(
+        _ptr(x), _ptr(out), _ptr(table.cos_sin), table.rows, table.rot_dim, int(table.interleaved),
+        _ptr(maps.tile_map), _ptr(maps.tile_valid), _ptr(pooled), B, N, H, D, maps.Npad, _stream(stream)))
+    return out, pooled
+
+
+def rotary_unpermute(x_t: torch.Tensor, table: RotaryTable, maps: DeviceMaps, N: int, inverse: bool = True,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """veda_rotary_unpermute: tiles back to raster order through the transposed rotation -- dQ / dK
+    of the attention's backward to the gradients of the unturned Q / K."""
+    _need(x_t, torch.bfloat16, "x_t")
+    if x_t.dim() != 4:
+        raise ValueError("x_t: expected shape [B, H, Npad, 128]")
+    B, H, Npad, D = x_t.shape
+    _need_maps(maps, H, Npad)
+    table._check()
+    if out is None:
+        out = _new((B, N, H, D), torch.bfloat16, x_t.device, stream)
+    _need(out, torch.bfloat16, "out", shape=(B, N, H, D))
+    _separate(out, x_t, "x_t", False)
+    _check("veda_rotary_unpermute", lib().veda_rotary_unpermute(
+        _ptr(x_t), _ptr(out), _ptr(table.cos_sin), table.rows, table.rot_dim, int(table.interleaved),
+        int(bool(inverse)), _ptr(maps.tile_map), B, N, H, D, Npad, _stream(stream)))
+    return out
+
+
+@dataclasses.dataclass
+class NormStats:
+    """What a norm's backward needs of its forward: mean (layer norm) and 1 / deviation of every
+    row, fp32 [B, N]."""
+    mean: torch.Tensor
+    rstd: torch.Tensor
+
+
+@dataclasses.dataclass
+class NormGrads:
+    """Gradients of a norm and of what is fused with it; None where there is no such parameter.
+    dx: of the normed input; the parameters' in fp32."""
+    dx: torch.Tensor
+    dweight: Optional[torch.Tensor] = None   # [C]
+    dbias: Optional[torch.Tensor] = None     # [C]
+    dscale: Optional[torch.Tensor] = None    # [B, C]
+    dshift: Optional[torch.Tensor] = None    # [B, C]
+    dgate: Optional[torch.Tensor] = None     # [B, C]
+
+
+def _rows3(t: torch.Tensor, name: str, dtype=None, shape=None, written=False) -> torch.Tensor:
+    """[N, C] as [1, N, C], checked."""
+    t = t.unsqueeze(0) if t.dim() == 2 else t
+    _need_strided(t, name, 3, dtype, shape, written)
+    return t
+
+
+def _rows(t: Optional[torch.Tensor]):
+    if t is None:
+        return None
+    return ctypes.byref(_Rows(_ptr(t), t.stride(0), t.stride(1), _DTYPE[t.dtype]))
+
+
+def _vectors(B: int, C: int, weight, bias, gain, shift, gain_name: str, offset: float):
+    """Checked parameters of a norm: weight / bias [C] of one type, gain / shift [B, C] ([C] for
+    one sequence) of one type with any batch stride."""
+    for t, n in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need_strided(t, n, 1, None, (C,))
+    fix = lambda t: t.unsqueeze(0) if t is not None and t.dim() == 1 else t
+    gain, shift = fix(gain), fix(shift)
+    for t, n in ((gain, gain_name), (shift, "shift")):
+        if t is not None:
+            _need_strided(t, n, 2, None, (B, C))
+    for a, b, n in ((weight, bias, "weight and bias"), (gain, shift, f"{gain_name} and shift")):
+        if a is not None and b is not None and a.dtype != b.dtype:
+            raise TypeError(f"{n}: expected one type, got {a.dtype} and {b.dtype}")
+    kind = lambda a, b: _DTYPE[a.dtype] if a is not None else _DTYPE[b.dtype] if b is not None else 2
+    return _NormParams(_ptr(weight), _ptr(bias), _ptr(gain), _ptr(shift),
+                       gain.stride(0) if gain is not None else 0, shift.stride(0) if shift is not None else 0,
+                       kind(weight, bias), kind(gain, shift), offset)
+
+
+def _norm_kind(kind: str) -> int:
+    if kind not in _KIND:
+        raise ValueError(f"kind must be one of {sorted(_KIND)}, got {kind!r}")
+    return _KIND[kind]
+
+
+def _norm_fwd(x, residual, params, residual_scale, kind, eps, out_dtype, out, want_stats, stream):
+    flat = x.dim() == 2
+    x3 = _rows3(x, "x")
+    B, N, C = x3.shape
+    if residual is not None:
+        residual = _rows3(residual, "residual", out_dtype, x3.shape)
+    if out is None:
+        out = _new(tuple(x.shape), out_dtype, x.device, stream)
+    out3 = _rows3(out, "out", out_dtype, x3.shape, written=True)
+    _separate(out3, x3, "x", True)
+    _separate(out3, residual, "the residual", True)
+    stats = None
+    if want_stats:
+        stats = NormStats(_new((B, N), torch.float32, x.device, stream), _new((B, N), torch.float32, x.device, stream))
+    _check("veda_norm_fwd", lib().veda_norm_fwd(
+        _rows(x3), _rows(residual), _rows(out3), ctypes.byref(params), float(residual_scale),
+        _ptr(stats.mean) if stats else None, _ptr(stats.rstd) if stats else None, B, N, C, _norm_kind(kind),
+        float(eps), _stream(stream)))
+    return (out, stats) if want_stats else out
+
+
+def norm_modulate(x: torch.Tensor, scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None,
+                  weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, kind: str = "layer",
+                  eps: float = 1e-6, out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                  want_stats: bool = False, stream=None):
+    """The norm before a block (veda_norm_fwd): (norm(x) weight + bias) (1 + scale) + shift.
+
+    x [B, N, C] or [N, C] (any row strides); weight / bias [C]; scale / shift [B, C], one vector
+    per sequence (any batch stride: slices of one modulation vector will do); every one of them
+    optional. kind "layer", "rms" or "none". ``want_stats`` also returns the ``NormStats`` of
+    ``norm_modulate_bwd``. out_dtype: x's type, or bf16 for fp32 x, or fp32 for bf16 x."""
+    x3 = x.unsqueeze(0) if x.dim() == 2 else x
+    _need_strided(x3, "x", 3)
+    p = _vectors(x3.shape[0], x3.shape[2], weight, bias, scale, shift, "scale", 1.0)
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else x.dtype
+    return _norm_fwd(x, None, p, 0.0, kind, eps, dt, out, want_stats, stream)
+
+
+def norm_gate_add(o: torch.Tensor, residual: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                  weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, kind: str = "rms",
+                  eps: float = 1e-6, residual_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                  want_stats: bool = False, stream=None):
+    """The norm after a block and the residual sum (veda_norm_fwd):
+    residual_scale residual + gate (norm(o) weight + bias).
+
+    o: the block's output [B, N, C] or [N, C]; residual of the same shape, whose type the result
+    has (o's type, or fp32 with bf16 o, or bf16 with fp32 o); gate [B, C]. kind "none" gates o
+    itself. ``out`` may be the residual (in place)."""
+    o3 = o.unsqueeze(0) if o.dim() == 2 else o
+    _need_strided(o3, "o", 3)
+    p = _vectors(o3.shape[0], o3.shape[2], weight, bias, gate, None, "gate", 0.0)
+    return _norm_fwd(o, residual, p, residual_scale, kind, eps, residual.dtype, out, want_stats, stream)
+
+
+def _norm_bwd(dy, x, stats, params, has, residual_grad, residual_scale, kind, out, stream):
+    x3 = _rows3(x, "x")
+    B, N, C = x3.shape
+    dy3 = _rows3(dy, "dy", None, x3.shape)
+    res3 = None if residual_grad is None else _rows3(residual_grad, "residual_grad", x.dtype, x3.shape)
+    k = _norm_kind(kind)
+    if stats is None and k != 2:
+        raise ValueError("stats: the forward's statistics are needed (want_stats=True)")
+    if stats is not None:
+        _need(stats.rstd, torch.float32, "stats.rstd", shape=(B, N))
+        _need(stats.mean, torch.float32, "stats.mean", shape=(B, N))
+    if out is None:
+        out = _new(tuple(x.shape), x.dtype, x.device, stream)
+    out3 = _rows3(out, "out", x.dtype, x3.shape, written=True)
+    for t, n in ((x3, "x"), (dy3, "dy"), (res3, "residual_grad")):
+        _separate(out3, t, n, True)
+    f32 = lambda want, *shape: _new(shape, torch.float32, x.device, stream) if want else None
+    dgain, dshift = f32(has["gain"], B, C), f32(has["shift"], B, C)
+    dweight, dbias = f32(has["weight"], C), f32(has["bias"], C)
+    nbytes = int(lib().veda_norm_bwd_workspace_bytes(B, N, C))
+    work = _new((max(nbytes, 16),), torch.uint8, x.device, stream)
+    _check("veda_norm_bwd", lib().veda_norm_bwd(
+        _rows(dy3), _rows(x3), _ptr(stats.mean) if stats else None, _ptr(stats.rstd) if stats else None,
+        _rows(res3), _rows(out3), ctypes.byref(params), float(residual_scale), _ptr(dgain), _ptr(dshift),
+        _ptr(dweight), _ptr(dbias), _ptr(work), work.numel(), B, N, C, k, _stream(stream)))
+    return out, dgain, dshift, dweight, dbias
+
+
+def norm_modulate_bwd(dy: torch.Tensor, x: torch.Tensor, stats: Optional[NormStats],
+                      scale: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, kind: str = "layer", want_dshift: bool = True,
+                      residual_grad: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+                      out: Optional[torch.Tensor] = None, stream=None) -> NormGrads:
+    """Backward of ``norm_modulate``: dx (x's type), dscale, dshift, dweight, dbias.
+
+    residual_grad (x's type) is the gradient of the stream that passes the block by: dx gets
+    residual_scale times it added, which saves the separate sum."""
+    x3 = x.unsqueeze(0) if x.dim() == 2 else x
+    _need_strided(x3, "x", 3)
+    p = _vectors(x3.shape[0], x3.shape[2], weight, bias, scale, None, "scale", 1.0)
+    has = dict(gain=scale is not None, shift=want_dshift, weight=weight is not None, bias=bias is not None)
+    dx, dg, dt, dw, db = _norm_bwd(dy, x, stats, p, has, residual_grad, residual_scale, kind, out, stream)
+    return NormGrads(dx, dw, db, dscale=dg, dshift=dt)
+
+
+def norm_gate_add_bwd(dh: torch.Tensor, o: torch.Tensor, stats: Optional[NormStats],
+                      gate: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, kind: str = "rms", out: Optional[torch.Tensor] = None,
+                      stream=None) -> NormGrads:
+    """Backward of ``norm_gate_add``: dx is the gradient of the block's output o, and dgate,
+    dweight, dbias. The residual's gradient is residual_scale dh, which ``norm_modulate_bwd`` of
+    the same block adds on its way (residual_grad=dh)."""
+    o3 = o.unsqueeze(0) if o.dim() == 2 else o
+    _need_strided(o3, "o", 3)
+    p = _vectors(o3.shape[0], o3.shape[2], weight, bias, gate, None, "gate", 0.0)
+    has = dict(gain=gate is not None, shift=False, weight=weight is not None, bias=bias is not None)
+    dx, dg, _, dw, db = _norm_bwd(dh, o, stats, p, has, None, 0.0, kind, out, stream)
+    return NormGrads(dx, dw, db, dgate=dg)
+
+
+@dataclasses.dataclass
+class Int8Rows:
+    """Rows of 8-bit codes with a scale each: codes int8 [rows, kp], kp = K rounded up to a
+    multiple of 16 with zeros behind K; scale fp32 [rows]; row r stands for codes * scale[r]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    K: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @staticmethod
+    def from_codes(codes: torch.Tensor, scale: torch.Tensor) -> "Int8Rows":
+        """From int8 codes [rows, K] made elsewhere (a checkpoint) and their scales [rows]."""
+        if codes.dim() != 2 or codes.dtype != torch.int8:
+            raise TypeError("codes: expected int8 [rows, K]")
+        rows, K = codes.shape
+        if tuple(scale.shape) != (rows,):
+            raise ValueError(f"scale: expected shape {(rows,)}, got {tuple(scale.shape)}")
+        kp = -(-K // 16) * 16
+        padded = codes.contiguous() if kp == K else torch.zeros((rows, kp), dtype=torch.int8, device=codes.device)
+        if kp != K:
+            padded[:, :K] = codes
+        return Int8Rows(padded, scale.float().contiguous(), K)
+
+    def _check(self, name: str) -> None:
+        if self.K <= 0:
+            raise ValueError(f"{name}: K must be positive")
+        _need(self.codes, torch.int8, f"{name}.codes", shape=(self.codes.shape[0], -(-self.K // 16) * 16))
+        _need(self.scale, torch.float32, f"{name}.scale", shape=(self.codes.shape[0],))
+
+
+def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
+    """x [..., K] as a matrix of rows without a copy."""
+    if x.dim() < 1:
+        raise ValueError(f"{name}: expected at least one dimension")
+    try:
+        return x.view(-1, x.shape[-1]) if x.numel() else x.reshape(0, x.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}: its leading dimensions do not form rows of one stride") from None
+
+
+def quantize_int8(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) -> Int8Rows:
+    """veda_quantize_int8: rows of x [..., K] (bf16, fp16 or fp32) to codes with a scale for each
+    row -- tokens of an activation, output channels of a weight [N, K]."""
+    m = _matrix(x, "x")
+    _need_strided(m, "x", 2)
+    rows, K = m.shape
+    kp = -(-K // 16) * 16
+    if out is None:
+        out = Int8Rows(_new((rows, kp), torch.int8, x.device, stream), _new((rows,), torch.float32, x.device, stream), K)
+    if out.K != K or out.rows != rows:
+        raise ValueError(f"out: expected {rows} rows of {K} codes")
+    out._check("out")
+    _check("veda_quantize_int8", lib().veda_quantize_int8(
+        _ptr(m), m.stride(0), _DTYPE[m.dtype], _ptr(out.codes), _ptr(out.scale), rows, K, _stream(stream)))
+    return out
+
+
+def int8_matmul(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
+                out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """veda_int8_matmul: y[m, n] = (a[m] . w[n]) a.scale[m] w.scale[n] + bias[n] (bias fp32 [N]);
+    y [M, N] in bf16, fp16 or fp32."""
+    a._check("a")
+    w._check("w")
+    if a.K != w.K:
+        raise ValueError(f"a has rows of {a.K} codes, w of {w.K}")
+    M, N = a.rows, w.rows
+    if bias is not None:
+        _need(bias, torch.float32, "bias", shape=(N,))
+    if out is None:
+        out = _new((M, N), out_dtype, a.codes.device, stream)
+    _need_strided(out, "out", 2, None, (M, N), written=True)
+    for t, n in ((a.codes, "a.codes"), (w.codes, "w.codes"), (a.scale, "a.scale"), (w.scale, "w.scale"), (bias, "bias")):
+        _separate(out, t, n, False)
+    _check("veda_int8_matmul", lib().veda_int8_matmul(
+        _ptr(a.codes), _ptr(a.scale), _ptr(w.codes), _ptr(w.scale), _ptr(bias), _ptr(out),
+        out.stride(0), _DTYPE[out.dtype], M, N, a.K, _stream(stream)))
+    return out
+
+
+def int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """x [..., K] W^T + bias in 8-bit integers: ``quantize_int8`` of x's rows, ``int8_matmul`` with
+    the weight's rows; [..., N] in x's type (or out_dtype)."""
+    a = quantize_int8(x, stream=stream)
+    y = int8_matmul(a, w, bias, out_dtype or x.dtype, stream=stream)
+    return y.view(*x.shape[:-1], w.rows)
+
+
 def check_device_status(stream=None) -> int:
     """Synchronise the stream and raise if a kernel recorded an error. Returns the raw bits."""
     detail = ctypes.c_uint32(0)
@@ -643,18 +1169,24 @@ class PathBuffers:
 
 def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: torch.Tensor,
                      wk: torch.Tensor, maps: DeviceMaps, rho: Sequence[Tuple[int, int]],
-                     scale: float, buffers: Optional[PathBuffers] = None, stream=None):
+                     scale: float, buffers: Optional[PathBuffers] = None, stream=None,
+                     rotary: Optional[RotaryTable] = None):
     """All six steps on raster Q/K/V [B, N, H, 128] (bf16, on the device).
 
     Returns the PathBuffers holding every intermediate; ``.o`` is the raster output. Steps 1
     and 2 of Q and K run as one call each (``permute_pool``: the tiles of ``permute_tiles``,
     the pooled features of ``tile_pool`` up to fp32 summation order in the mean), so that the
-    tiled Q and K are not read a second time.
+    tiled Q and K are not read a second time. ``rotary``: positions turned into Q and K on the
+    way into the tiles (``rotary_permute_pool``).
     """
     B, N, H, D = q.shape
     bufs = buffers or PathBuffers.allocate(B, N, H, maps, rho, q.device)
-    permute_pool(q, maps, bufs.q_t, bufs.pooled_q, stream)
-    permute_pool(k, maps, bufs.k_t, bufs.pooled_k, stream)
+    if rotary is None:
+        permute_pool(q, maps, bufs.q_t, bufs.pooled_q, stream)
+        permute_pool(k, maps, bufs.k_t, bufs.pooled_k, stream)
+    else:
+        rotary_permute_pool(q, rotary, maps, bufs.q_t, bufs.pooled_q, stream)
+        rotary_permute_pool(k, rotary, maps, bufs.k_t, bufs.pooled_k, stream)
     permute_tiles(v, maps, bufs.v_t, stream)
     block_scores(bufs.pooled_q, bufs.pooled_k, wq, wk, bufs.scores, bufs.workspace, stream)
     select_blocks(bufs.scores, maps, rho, bufs.lists.stride, bufs.lists, stream)
@@ -662,6 +1194,56 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: torc
                           bufs.lse, stream=stream)
     unpermute(bufs.o_t, maps, N, bufs.o, stream)
     return bufs
+
+
+@dataclasses.dataclass
+class BlockWeights:
+    """Weights of one attention block: 8-bit projections (rows are output channels; H * 128 of Q,
+    K, V), the predictor's projections, and the norms around the block."""
+    q: Int8Rows
+    k: Int8Rows
+    v: Int8Rows
+    o: Int8Rows
+    pred_q: torch.Tensor                        # [H, 128, 384] fp32
+    pred_k: torch.Tensor
+    q_bias: Optional[torch.Tensor] = None       # fp32
+    k_bias: Optional[torch.Tensor] = None
+    v_bias: Optional[torch.Tensor] = None
+    o_bias: Optional[torch.Tensor] = None
+    pre_weight: Optional[torch.Tensor] = None   # norm before the block
+    pre_bias: Optional[torch.Tensor] = None
+    post_weight: Optional[torch.Tensor] = None  # norm after it
+    pre_kind: str = "layer"
+    post_kind: str = "none"
+    eps: float = 1e-6
+
+
+def attention_block(x: torch.Tensor, w: BlockWeights, scale: Optional[torch.Tensor], shift: Optional[torch.Tensor],
+                    gate: Optional[torch.Tensor], table: RotaryTable, maps: DeviceMaps,
+                    rho: Sequence[Tuple[int, int]], softmax_scale: float, residual_scale: float = 1.0,
+                    buffers: Optional[PathBuffers] = None, stream=None) -> torch.Tensor:
+    """One self-attention block on the residual stream x [B, N, C] (bf16 or fp32), for inference:
+
+    ``norm_modulate`` (scale, shift), one ``quantize_int8`` for the three ``int8_matmul`` of Q, K and
+    V, ``sparse_attention`` with the rotary positions, ``int8_linear`` back to C channels, and
+    ``norm_gate_add`` (gate, residual). Returns the new stream, of x's type."""
+    if x.dim() != 3:
+        raise ValueError("x: expected shape [B, N, C]")
+    B, N, C = x.shape
+    H = w.pred_q.shape[0]
+    for r, n in ((w.q, "q"), (w.k, "k"), (w.v, "v")):
+        if r.rows != H * 128:
+            raise ValueError(f"{n}: expected {H * 128} output channels, got {r.rows}")
+    a = norm_modulate(x, scale, shift, w.pre_weight, w.pre_bias, w.pre_kind, w.eps, torch.bfloat16, stream=stream)
+    a8 = quantize_int8(a, stream=stream)
+    q, k, v = (int8_matmul(a8, r, b, stream=stream).view(B, N, H, 128)
+               for r, b in ((w.q, w.q_bias), (w.k, w.k_bias), (w.v, w.v_bias)))
+    if buffers is None and stream is not None:
+        with torch.cuda.stream(stream):
+            buffers = PathBuffers.allocate(B, N, H, maps, rho, x.device)
+    bufs = sparse_attention(q, k, v, w.pred_q, w.pred_k, maps, rho, softmax_scale, buffers, stream, rotary=table)
+    o = int8_linear(bufs.o.view(B, N, H * 128), w.o, w.o_bias, stream=stream)
+    return norm_gate_add(o, x, gate, w.post_weight, None, w.post_kind, w.eps, residual_scale, stream=stream)
 
 
 class HostPipeline:

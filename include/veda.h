@@ -28,6 +28,15 @@
  *   veda_quantize_fp8              tiled bf16 -> e4m3 codes with one scale per (batch, head)
  *   veda_block_sparse_attn_fwd_fp8 step 5 with e4m3 Q / K / V and e4m3 P on the tensor cores
  *
+ * and the operators of the transformer block around the attention (this library's):
+ *
+ *   veda_rotary_table, veda_rotary rotary positions of Q and K
+ *   veda_rotary_permute_pool       steps 1 + 2 with the rotation on the way
+ *   veda_rotary_unpermute          step 6 with a rotation on the way (the gradients' way back)
+ *   veda_norm_fwd, veda_norm_bwd   the norms before and after a block with its scale, shift,
+ *                                  gate and residual sum
+ *   veda_quantize_int8, veda_int8_matmul  projections in 8-bit integers
+ *
  * Conventions shared by every call:
  *  - Ownership: the caller allocates and owns every buffer. Pointers named *_dev or
  *    documented as "device" must be device memory of the current CUDA device; the
@@ -489,6 +498,171 @@ VEDA_API veda_status veda_tile_plan_vote(const double* errors, int32_t H, int32_
  * VEDA_ERR_TIMEOUT (site 0xEE in the detail bits) and the context stays usable.
  */
 VEDA_API veda_status veda_selftest_wait_timeout(uint32_t limit_us, veda_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * The transformer block around the attention: rotary positions of Q and K, the norms before
+ * and after the block, and 8-bit integer projections (this library's, defined by the formulas
+ * below). They take strided tensors and several types; sizes of zero (no token, no row) are
+ * valid and launch nothing. Strides are in elements; channels are contiguous.
+ * ---------------------------------------------------------------------------------------
+ */
+#define VEDA_BF16 0
+#define VEDA_FP16 1
+#define VEDA_FP32 2
+
+/*
+ * Table of rotary positions (device):
+ *   cos_sin[r][p] = amplitude * (cos, sin)(positions[axis[p]][r] * inv_freq[p])
+ * with the angle, its sine and its cosine in fp64, rounded once to fp32.
+ *   positions   [axes][rows] int32 (device); any values
+ *   inv_freq    [pairs] double (HOST), axis [pairs] int32 (HOST) in [0, axes)
+ *   cos_sin     [rows][pairs][2] fp32 (device, out), 16-byte aligned
+ * Limits: 1 <= pairs <= 256, 1 <= axes <= 8. Scalings for long contexts change inv_freq and
+ * amplitude only.
+ */
+VEDA_API veda_status veda_rotary_table(const int32_t* positions, int32_t axes, int64_t rows,
+                                       const double* inv_freq, const int32_t* axis, int32_t pairs,
+                                       double amplitude, float* cos_sin, veda_stream_t stream);
+
+/*
+ * Rotary positions of a raster tensor (device). With P = rot_dim / 2 and (c, s) the table's row
+ * of the token:
+ *   interleaved:  (x[2p], x[2p+1])  -> (x[2p] c_p - x[2p+1] s_p, x[2p+1] c_p + x[2p] s_p)
+ *   half layout:  (x[p], x[p+P])    -> the same pairs, P channels apart
+ * Channels from rot_dim on are copied. inverse != 0 turns by -s (the transpose: the gradient's
+ * way back). fp32 arithmetic, one rounding per result.
+ *   x, y          [B][N][H][D] of `dtype` with element strides x_strides / y_strides
+ *                 {batch, token, head} (HOST); y may be x (same strides), else no overlap
+ *   cos_sin       [table_rows][P][2] fp32 (device), 16-byte aligned
+ *   rows          NULL or [B][N] int32 (device): table row of each token. NULL: row n of every
+ *                 sequence (table_rows == N) or row b * N + n (table_rows == B * N). A row
+ *                 outside the table is flagged VEDA_ERR_DEVICE_CHECK and its token is written
+ *                 as zeros
+ * Limits: rot_dim even, 2 <= rot_dim <= min(D, 512), D <= 1024.
+ */
+VEDA_API veda_status veda_rotary(const void* x, const int64_t* x_strides, void* y, const int64_t* y_strides,
+                                 int32_t dtype, const float* cos_sin, int64_t table_rows,
+                                 const int32_t* rows, int32_t rot_dim, int32_t interleaved,
+                                 int32_t inverse, int32_t B, int32_t N, int32_t H, int32_t D,
+                                 veda_stream_t stream);
+
+/*
+ * veda_permute_pool with the rotation of veda_rotary on the way (device): x is read once, the
+ * rotated tiles are written once. x_tiled is bit-identical to rotating first; the pooled mean /
+ * max / min are those of the rotated fp32 values before they are rounded to bf16.
+ *   cos_sin, table_rows  as veda_rotary without rows (table_rows N or B * N, by raster token)
+ *   rot_dim              multiple of 16, 16 <= rot_dim <= 128
+ *   everything else      as veda_permute_pool
+ */
+VEDA_API veda_status veda_rotary_permute_pool(const void* x, void* x_tiled, const float* cos_sin,
+                                              int64_t table_rows, int32_t rot_dim, int32_t interleaved,
+                                              const int32_t* tile_map, const int32_t* tile_valid,
+                                              float* pooled, int32_t B, int32_t N, int32_t H, int32_t D,
+                                              int32_t Npad, veda_stream_t stream);
+
+/*
+ * veda_unpermute with a rotation on the way (device). inverse != 0 is the transpose of
+ * veda_rotary_permute_pool's tiles: it takes dQ or dK in tile order to the gradient of the
+ * unrotated raster tensor. Arguments as veda_unpermute and veda_rotary_permute_pool.
+ */
+VEDA_API veda_status veda_rotary_unpermute(const void* x_tiled, void* x, const float* cos_sin,
+                                           int64_t table_rows, int32_t rot_dim, int32_t interleaved,
+                                           int32_t inverse, const int32_t* tile_map, int32_t B,
+                                           int32_t N, int32_t H, int32_t D, int32_t Npad,
+                                           veda_stream_t stream);
+
+/* Rows of a [B][N][C] tensor (device): element strides of the batch and of the row. */
+typedef struct veda_rows {
+  void* data;
+  int64_t batch_stride, row_stride;
+  int32_t dtype;
+} veda_rows;
+
+#define VEDA_NORM_LAYER 0   /* xh = (x - mean) / sqrt(var + eps), biased variance */
+#define VEDA_NORM_RMS 1     /* xh = x / sqrt(mean(x^2) + eps) */
+#define VEDA_NORM_NONE 2    /* xh = x */
+
+/*
+ * Parameters of a norm and of what is fused with it (device pointers, any may be NULL):
+ *   weight, bias   [C] of weight_dtype (NULL: 1 and 0)
+ *   gain, shift    [B][C] of mod_dtype, rows gain_stride / shift_stride elements apart
+ *   gain_offset    G = gain_offset + gain (1 for a scale, 0 for a gate); G = 1 without gain
+ */
+typedef struct veda_norm_params {
+  const void *weight, *bias, *gain, *shift;
+  int64_t gain_stride, shift_stride;
+  int32_t weight_dtype, mod_dtype;
+  float gain_offset;
+} veda_norm_params;
+
+/*
+ * Norm before or after a block (device):
+ *   y[b][n] = residual_scale * residual[b][n] + G[b] * (xh * weight + bias) + shift[b]
+ * Before the block: G = 1 + scale, no residual. After it: G = gate, residual the stream.
+ *   x, y, residual  rows of C channels; x and y of one type, or bf16 and fp32 either way;
+ *                   residual (or NULL) of y's type. y may be x or residual row for row
+ *   mean, rstd      NULL or [B][N] fp32 (device, out): the statistics the backward needs (mean
+ *                   only for the layer norm; 0 and 1 where the kind has none)
+ * Statistics are fp32, the variance from the centred values; one rounding to y's type.
+ * Limits: 1 <= C <= 8192, eps >= 0.
+ */
+VEDA_API veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const veda_rows* y,
+                                   const veda_norm_params* params, float residual_scale, float* mean,
+                                   float* rstd, int32_t B, int32_t N, int32_t C, int32_t kind, float eps,
+                                   veda_stream_t stream);
+
+/* Workspace bytes of veda_norm_bwd. */
+VEDA_API size_t veda_norm_bwd_workspace_bytes(int32_t B, int32_t N, int32_t C);
+
+/*
+ * Backward of veda_norm_fwd (device). For the output gradient dy, with g = dy * G * weight:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + residual_scale * residual_grad
+ * (rms: without mean(g); none: dx = g + ...). residual_grad (or NULL) is the gradient that
+ * reaches x around the block. With sums over the tokens of a sequence, and over all tokens:
+ *   dgain[b] = sum dy (xh weight + bias)    dshift[b] = sum dy        ([B][C] fp32, or NULL)
+ *   dweight = sum dy G xh                   dbias = sum dy G          ([C] fp32, or NULL)
+ * The gradient of the forward's residual is residual_scale * dy.
+ *   dy          rows of the forward's y type; x, dx, residual_grad rows of its x type;
+ *               dx may be dy (same type), x or residual_grad row for row
+ *   mean, rstd  [B][N] fp32 of the forward
+ *   workspace   device scratch of >= veda_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ * Sums are fp32, per slice of a sequence and then over the slices in a fixed order: results do
+ * not change from run to run. B <= 65535.
+ */
+VEDA_API veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* mean, const float* rstd,
+                                   const veda_rows* residual_grad, const veda_rows* dx,
+                                   const veda_norm_params* params, float residual_scale, float* dgain,
+                                   float* dshift, float* dweight, float* dbias, void* workspace,
+                                   size_t workspace_bytes, int32_t B, int32_t N, int32_t C, int32_t kind,
+                                   veda_stream_t stream);
+
+/*
+ * Rows to 8-bit integers (device): scale[r] = fp32(max |x_r| / 127), codes = x / scale rounded
+ * to the nearest integer, ties to even, exactly. A row whose largest |x| is below 2^-100 gets
+ * scale 1 and codes 0; a row with a NaN or an infinity gets scale NaN and codes 0, so that
+ * everything computed from it is NaN. The same call lays out activations (a row per token) and
+ * weights (a row per output channel).
+ *   x        [rows][K] of `dtype`, rows x_stride elements apart
+ *   codes    [rows][kp] int8 (device, out), kp = K rounded up to a multiple of 16, zeros behind
+ *            K; 16-byte aligned
+ *   scale    [rows] fp32 (device, out)
+ */
+VEDA_API veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t dtype, void* codes,
+                                        float* scale, int64_t rows, int32_t K, veda_stream_t stream);
+
+/*
+ * Product of 8-bit integers (device):
+ *   y[m][n] = (sum_k a[m][k] w[n][k]) * (a_scale[m] * w_scale[n]) + bias[n]
+ * The sum is exact (32-bit integers); it is rounded to fp32 once, and y once to its type.
+ *   a, w      [M][kp], [N][kp] int8 codes as veda_quantize_int8 stores them, 16-byte aligned
+ *   bias      NULL or [N] fp32
+ *   y         [M][N] of `dtype` (device, out), rows y_stride elements apart
+ * Limits: K <= 131071 (128 * 128 * K stays below 2^31).
+ */
+VEDA_API veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w, const float* w_scale,
+                                      const float* bias, void* y, int64_t y_stride, int32_t dtype, int32_t M,
+                                      int32_t N, int32_t K, veda_stream_t stream);
 
 /*
  * Synchronise `stream`, then read and clear the current device's status word.

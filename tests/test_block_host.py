@@ -1,0 +1,205 @@
+"""Block operators without a GPU: argument checks at the C ABI (before any CUDA call) and in the
+binding, and the host-side rotary frequencies and positions."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+veda = pytest.importorskip("block_sparse_attention_max_b200.veda")
+OK, INVALID, UNSUPPORTED = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    from block_sparse_attention_max_b200 import build
+    build.build()
+    return veda.lib()
+
+
+def _i64(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def test_rotary_table_refusals(L):
+    inv, ax = (ctypes.c_double * 4)(1, .1, .01, .001), (ctypes.c_int32 * 4)(0, 0, 1, 1)
+    call = lambda pos=16, axes=2, rows=8, i=inv, a=ax, pairs=4, amp=1.0, out=16: L.veda_rotary_table(
+        pos, axes, rows, ctypes.addressof(i) if i is not None else None, ctypes.addressof(a) if a is not None else None,
+        pairs, amp, out, None)
+    for bad in (dict(axes=0), dict(axes=9), dict(axes=1), dict(rows=-1), dict(pairs=0), dict(pairs=257), dict(i=None),
+                dict(a=None), dict(amp=math.inf), dict(pos=None), dict(out=None), dict(out=8), dict(pos=2),
+                dict(i=(ctypes.c_double * 4)(1, math.nan, 0, 0)), dict(a=(ctypes.c_int32 * 4)(0, 0, 0, -1))):
+        assert call(**bad) == INVALID, bad
+        assert L.veda_last_error()
+    assert call(rows=0) == OK and call(rows=0, pos=None, out=None) == OK
+
+
+def test_rotary_refusals(L):
+    st = _i64(4096, 512, 128)
+
+    def call(x=256, y=512, dtype=0, cs=16, trows=8, rows=None, rot=128, B=1, N=8, H=4, D=128, xs=st, ys=st):
+        return L.veda_rotary(x, ctypes.addressof(xs) if xs is not None else None, y,
+                             ctypes.addressof(ys) if ys is not None else None, dtype, cs, trows, rows, rot, 1, 0, B,
+                             N, H, D, None)
+    for bad in (dict(x=None), dict(y=None), dict(cs=None), dict(cs=8), dict(dtype=3), dict(dtype=-1), dict(trows=7),
+                dict(trows=9), dict(B=-1), dict(N=-1), dict(H=-1), dict(D=0), dict(xs=None), dict(ys=None),
+                dict(x=255), dict(rows=6), dict(rows=16, trows=0), dict(dtype=2, x=258)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(rot=0), dict(rot=130), dict(rot=63), dict(D=1032), dict(D=640, rot=514)):
+        assert call(**bad) == UNSUPPORTED, bad
+    assert call(N=0, trows=0, x=None, y=None) == OK and call(H=0) == OK
+
+
+def test_rotary_tile_refusals(L):
+    def pool(x=256, xt=512, cs=16, trows=256, rot=128, m=16, v=16, p=16, B=1, N=256, H=1, D=128, Npad=256):
+        return L.veda_rotary_permute_pool(x, xt, cs, trows, rot, 1, m, v, p, B, N, H, D, Npad, None)
+
+    def back(x=256, xt=512, cs=16, trows=256, rot=128, m=16, B=1, N=256, H=1, D=128, Npad=256):
+        return L.veda_rotary_unpermute(xt, x, cs, trows, rot, 1, 1, m, B, N, H, D, Npad, None)
+    for f in (pool, back):
+        for bad in (dict(x=None), dict(xt=None), dict(m=None), dict(cs=None), dict(cs=4), dict(x=8), dict(xt=8),
+                    dict(trows=255), dict(trows=512), dict(B=0), dict(N=0), dict(H=0), dict(Npad=100), dict(m=2)):
+            assert f(**bad) == INVALID, bad
+        for bad in (dict(D=64), dict(rot=8), dict(rot=144), dict(rot=24)):
+            assert f(**bad) == UNSUPPORTED, bad
+    assert pool(v=None) == INVALID and pool(p=None) == INVALID and pool(p=8) == INVALID
+
+
+def _rows(data=256, b=640, r=64, dtype=0):
+    return ctypes.byref(veda._Rows(data, b, r, dtype))
+
+
+def _params(**k):
+    d = dict(weight=None, bias=None, gain=None, shift=None, gain_stride=0, shift_stride=0, weight_dtype=2, mod_dtype=2,
+             gain_offset=1.0)
+    d.update(k)
+    return ctypes.byref(veda._NormParams(*[d[f] for f, _ in veda._NormParams._fields_]))
+
+
+def test_norm_refusals(L):
+    def fwd(x=None, res=None, y=None, p=None, mean=None, rstd=None, B=1, N=10, C=64, kind=0, eps=1e-6):
+        return L.veda_norm_fwd(x or _rows(), res, y or _rows(512), p or _params(), 1.0, mean, rstd, B, N, C, kind, eps,
+                               None)
+    for bad in (dict(B=-1), dict(N=-1), dict(N=2**31 - 1), dict(C=0), dict(kind=3), dict(kind=-1), dict(eps=-1.0),
+                dict(eps=math.nan), dict(x=_rows(dtype=5)), dict(x=_rows(None)), dict(x=_rows(257)), dict(y=_rows(None)),
+                dict(mean=16), dict(rstd=2), dict(res=_rows(256, dtype=2)), dict(res=_rows(None)),
+                dict(p=_params(weight=16, weight_dtype=7)), dict(p=_params(gain=18))):
+        assert fwd(**bad) == INVALID, bad
+    assert fwd(C=8193) == UNSUPPORTED
+    assert fwd(x=_rows(dtype=1)) == UNSUPPORTED and fwd(y=_rows(dtype=1)) == UNSUPPORTED   # fp16 with another type
+    assert fwd(B=0) == OK and fwd(N=0, x=_rows(None), y=_rows(None)) == OK
+    assert L.veda_norm_fwd(None, None, _rows(), _params(), 1.0, None, None, 1, 1, 8, 0, 1e-6, None) == INVALID
+
+    need = L.veda_norm_bwd_workspace_bytes(1, 10, 64)
+    assert need > 0 and L.veda_norm_bwd_workspace_bytes(0, 1, 1) == 0 == L.veda_norm_bwd_workspace_bytes(1, 1, 8193)
+
+    def bwd(dy=None, x=None, mean=16, rstd=16, res=None, dx=None, dg=None, ws=16, nws=need, B=1, N=10, C=64, kind=0):
+        return L.veda_norm_bwd(dy or _rows(), x or _rows(), mean, rstd, res, dx or _rows(512), _params(), 1.0, dg,
+                               None, None, None, ws, nws, B, N, C, kind, None)
+    for bad in (dict(mean=None), dict(rstd=None), dict(kind=1, rstd=None), dict(ws=None), dict(ws=8),
+                dict(nws=need - 1), dict(dx=_rows(dtype=2)), dict(res=_rows(dtype=2)), dict(dg=2), dict(dy=_rows(None)),
+                dict(x=_rows(None)), dict(C=0), dict(kind=7)):
+        assert bwd(**bad) == INVALID, bad
+    assert bwd(B=70000, nws=2**60) == UNSUPPORTED
+
+
+def test_norm_workspace_covers_every_slice_count(L):
+    """B sequences are cut into ceil(160 SMs * 4 / B) slices at most, none of them empty."""
+    for B in (1, 2, 3, 7, 64, 639, 640, 641, 1500, 65535):
+        for N in (1, 2, 5, 1000, 100000):
+            slices = max(1, min(-(-640 // B), N))
+            assert L.veda_norm_bwd_workspace_bytes(B, N, 100) >= (B * slices + B) * 2 * 100 * 4
+
+
+def test_int8_refusals(L):
+    q = lambda x=256, st=64, dt=0, c=16, s=16, rows=4, K=64: L.veda_quantize_int8(x, st, dt, c, s, rows, K, None)
+    for bad in (dict(x=None), dict(c=None), dict(s=None), dict(c=8), dict(s=2), dict(x=255), dict(dt=3), dict(rows=-1),
+                dict(rows=2**31), dict(K=0), dict(K=2**31 - 8)):
+        assert q(**bad) == INVALID, bad
+    assert q(rows=0, x=None) == OK
+
+    def mm(a=16, sa=16, w=16, sw=16, bias=None, y=16, ys=32, dt=0, M=4, N=32, K=64):
+        return L.veda_int8_matmul(a, sa, w, sw, bias, y, ys, dt, M, N, K, None)
+    for bad in (dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(y=None), dict(a=8), dict(w=8),
+                dict(sa=2), dict(sw=1), dict(bias=2), dict(y=17), dict(dt=4), dict(M=-1), dict(N=-1), dict(K=0),
+                dict(ys=31), dict(ys=-1)):
+        assert mm(**bad) == INVALID, bad
+    assert mm(K=131072) == UNSUPPORTED
+    assert mm(M=0) == OK and mm(N=0) == OK
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU behaviour")
+def test_no_device_means_error(L):
+    st = _i64(4096, 512, 128)
+    assert L.veda_rotary(256, ctypes.addressof(st), 512, ctypes.addressof(st), 0, 16, 8, None, 128, 1, 0, 1, 8, 4, 128,
+                         None) in (2, 3)
+    assert L.veda_int8_matmul(16, 16, 16, 16, None, 16, 32, 0, 4, 32, 64, None) in (2, 3)
+    assert L.veda_norm_fwd(_rows(), None, _rows(512), _params(), 1.0, None, None, 1, 10, 64, 0, 1e-6, None) in (2, 3)
+
+
+def test_binding_checks():
+    f = torch.float32
+    x = torch.zeros(1, 4, 2, 64)
+    for call in (lambda: veda.rotary(x, veda.RotaryTable(torch.zeros(4, 32, 2), True)),
+                 lambda: veda.norm_modulate(x[0, 0]), lambda: veda.quantize_int8(x),
+                 lambda: veda.rotary_table(torch.zeros(3, dtype=torch.int32), np.ones(2))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError):
+        veda._need_strided(torch.zeros(2, 2, dtype=torch.float64), "x", 2)
+    with pytest.raises(ValueError, match="dimensions"):
+        veda._need_strided(torch.zeros(2, 2), "x", 3)
+    with pytest.raises(ValueError, match="contiguous"):
+        veda._need_strided(torch.zeros(4, 4).t(), "x", 2)
+    with pytest.raises(ValueError, match="rows of one stride"):
+        veda._matrix(torch.zeros(4, 6, 8)[:, :3], "x")
+    assert veda._matrix(torch.zeros(4, 6, 16)[..., :8], "x").stride(0) == 16
+    a = torch.zeros(64)
+    with pytest.raises(ValueError, match="overlaps"):
+        veda._separate(a[1:33], a[:32], "x", True)
+    veda._separate(a[:32], a[32:], "x", True)
+    veda._separate(a[:32], a[:32], "x", True)
+    with pytest.raises(ValueError, match="must not be"):
+        veda._separate(a[:32], a[:32], "x", False)
+    with pytest.raises(ValueError, match="kind"):
+        veda._norm_kind("group")
+    with pytest.raises(TypeError):
+        veda.Int8Rows.from_codes(torch.zeros(2, 3), torch.ones(2))
+    with pytest.raises(ValueError, match="scale"):
+        veda.Int8Rows.from_codes(torch.zeros(2, 3, dtype=torch.int8), torch.ones(3))
+    r = veda.Int8Rows.from_codes(torch.ones(2, 3, dtype=torch.int8), torch.ones(2, dtype=f))
+    assert r.codes.shape == (2, 16) and r.codes.sum() == 6 and r.K == 3
+
+
+def test_frequencies():
+    f = veda.rotary_frequencies(128)
+    assert np.allclose(f.inv_freq, 10000.0 ** (-np.arange(64) / 64), rtol=1e-14) and (f.axis == 0).all()
+    f3 = veda.rotary_frequencies((44, 42, 42), theta=256.0)
+    assert len(f3.inv_freq) == 64 and list(np.bincount(f3.axis)) == [22, 21, 21]
+    assert f3.inv_freq[0] == f3.inv_freq[22] == f3.inv_freq[43] == 1.0 and f3.amplitude == 1.0
+    assert np.allclose(veda.rotary_frequencies(64, scaling="linear", factor=4).inv_freq,
+                       veda.rotary_frequencies(64).inv_freq / 4, rtol=1e-15)
+    base, ntk = veda.rotary_frequencies(64), veda.rotary_frequencies(64, scaling="ntk", factor=8)
+    assert ntk.inv_freq[0] == 1.0 and np.isclose(ntk.inv_freq[-1], base.inv_freq[-1] / 8, rtol=1e-12)
+    y = veda.rotary_frequencies(128, scaling="yarn", factor=4, original_length=4096)
+    base = veda.rotary_frequencies(128).inv_freq
+    turns = 4096 * base / (2 * np.pi)
+    ratio = y.inv_freq / base
+    assert (ratio[turns > 40] == 1).all() and np.allclose(ratio[turns < 0.8], 0.25)
+    assert (np.diff(ratio) <= 1e-15).all() and np.isclose(y.amplitude, 0.1 * math.log(4) + 1)
+    for scaling in ("linear", "ntk", "yarn"):                          # factor 1 changes nothing
+        g = veda.rotary_frequencies(128, scaling=scaling, factor=1.0, original_length=4096)
+        assert np.allclose(g.inv_freq, base, rtol=1e-14) and g.amplitude == 1.0
+    for bad in (dict(dims=3), dict(dims=()), dict(dims=(0, 0)), dict(dims=(4, -2)), dict(dims=8, theta=1.0),
+                dict(dims=8, scaling="x"), dict(dims=8, factor=0.5), dict(dims=2, scaling="ntk", factor=2),
+                dict(dims=8, scaling="yarn", factor=2), dict(dims=8, scaling="yarn", original_length=8, beta_slow=40)):
+        with pytest.raises(ValueError):
+            veda.rotary_frequencies(**bad)
+
+
+def test_positions():
+    p = veda.rotary_positions((2, 3, 4), 2)
+    assert p.shape == (3, 26) and p.dtype == np.int32
+    for n, thw in ((0, (0, 0, 0)), (5, (0, 1, 1)), (12, (1, 0, 0)), (23, (1, 2, 3)), (24, (4, 4, 4)), (25, (5, 5, 5))):
+        assert tuple(p[:, n]) == thw
