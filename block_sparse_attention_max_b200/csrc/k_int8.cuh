@@ -22,8 +22,8 @@ namespace int8 {
 // ------------------------------------------------------------------------------------
 // Row quantisation. A row belongs to a warp (K <= 1024) or to a CTA of 128 threads; it is held
 // in registers between the maximum and the rounding (rows over 8,192 are read again, from L2).
-// The division is exact: q = rint(x / scale approximately), then the sign of the exactly
-// rounded x - scale (q +- 1/2) tells whether q is the nearest integer, ties to even.
+// The division is exact: x * (1 / scale) is rounded, and where that product lies next to a half the
+// sign of the exactly rounded x - scale (q +- 1/2) decides, ties to even.
 // A row with a NaN or an infinity gets scale NaN (and codes 0), so its outputs are NaN; a row
 // whose largest value is below 2^-100 counts as zero (scale 1, codes 0).
 // ------------------------------------------------------------------------------------
@@ -56,26 +56,47 @@ __device__ __forceinline__ void load8(const T* row, int32_t k0, int32_t K, bool 
   }
 }
 
-// x / s to the nearest integer, ties to even, |x| <= 127.5 s.
+// x / s to the nearest integer, ties to even, |x| <= 127.5 s, for a quotient near a half-integer
+// (x * inv is off by less than 2^-15): fma rounds x - s (q +- 1/2) once, so its sign is exact.
 __device__ __forceinline__ int32_t div_round(float x, float s, float inv) {
-  const float t = x * inv;
-  float q = rintf(t);
-  // only a quotient within 2^-12 of a half-integer (the product is off by less than 2^-15) can
-  // need the exact test: fma rounds s (q +- 1/2) - x once, so its sign is exact
-  if (fabsf(t - q) > 0.49975586f) {
-    const float up = fmaf(-s, q + 0.5f, x), dn = fmaf(-s, q - 0.5f, x);
-    const bool odd = (static_cast<int32_t>(q) & 1) != 0;
-    if (up > 0.f || (up == 0.f && odd)) q += 1.f;
-    else if (dn < 0.f || (dn == 0.f && odd)) q -= 1.f;
-  }
+  float q = rintf(x * inv);
+  const float up = fmaf(-s, q + 0.5f, x), dn = fmaf(-s, q - 0.5f, x);
+  const bool odd = (static_cast<int32_t>(q) & 1) != 0;
+  if (up > 0.f || (up == 0.f && odd)) q += 1.f;
+  else if (dn < 0.f || (dn == 0.f && odd)) q -= 1.f;
   return static_cast<int32_t>(q);
 }
 
-__device__ __forceinline__ uint2 codes8(const float* f, float s, float inv, bool live) {
+// The eight codes of a vector by the exact test (out of line: it runs rarely).
+__device__ __noinline__ uint2 codes8_exact(float4 a, float4 b, float s, float inv) {
+  const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t w[2] = {0u, 0u};
-  if (live) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i >> 2] |= (static_cast<uint32_t>(div_round(f[i], s, inv)) & 0xffu) << (8 * (i & 3));
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= (static_cast<uint32_t>(div_round(f[i], s, inv)) & 0xffu) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+// Eight codes. Adding 1.5 * 2^23 to x * inv rounds it to an integer, ties to even, whose low byte
+// is the float's; d is what was rounded away. Only where some |d| is within 2^-14 of a half can an
+// integer be the wrong neighbour, and only then (1 vector in 500 or so) is the exact test run.
+__device__ __forceinline__ uint2 codes8(const float* f, float s, float inv, bool live) {
+  if (!live) return make_uint2(0u, 0u);
+  constexpr float kRound = 12582912.0f;
+  float t[8];
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = fmaf(f[i], inv, kRound);
+    worst = fmaxf(worst, fabsf(fmaf(f[i], inv, kRound - t[i])));
+  }
+  if (worst > 0.5f - 0x1p-14f)
+    return codes8_exact(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]), s, inv);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __byte_perm(__float_as_uint(t[4 * h]), __float_as_uint(t[4 * h + 1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(t[4 * h + 2]), __float_as_uint(t[4 * h + 3]), 0x0040);
+    w[h] = __byte_perm(lo, hi, 0x5410);
   }
   return make_uint2(w[0], w[1]);
 }

@@ -47,6 +47,7 @@ struct Param {                     // a parameter vector of C values, with a bat
   const void* p;
   int64_t bs;
   int32_t dtype;
+  int32_t vec;                     // its rows start on 16-byte boundaries and C % 8 == 0
 };
 
 struct Args {
@@ -62,7 +63,6 @@ struct Args {
   float* part;                     // backward: [B * slices][2][C] partial P1, P2
   int32_t B, N, C, kind, slices;
   int32_t stages;                  // rows in the ring: 2 to 4
-  int32_t vec;                     // every row starts on a 16-byte boundary and C % 8 == 0
 };
 
 __device__ __forceinline__ float load_param(const Param& q, int32_t b, int32_t c) {
@@ -84,13 +84,6 @@ template <> __device__ __forceinline__ float from_f<float>(float v) { return v; 
 // One 8-channel vector of T in 16-byte units: 1 (16-bit types) or 2 (fp32).
 template <typename T> constexpr int units_of() { return sizeof(T) * kVec / 16; }
 
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4* u, float* f) {
-  const T* p = reinterpret_cast<const T*>(u);
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) f[i] = to_f<T>(p[i]);
-}
-
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -108,59 +101,188 @@ __device__ __forceinline__ void wait_oldest(int32_t stages) {
   else cp_async_wait<0>();
 }
 
-// This thread's share of a row of T into its own ring slots (slot stride: `threads` units).
-template <typename T, int NV>
-__device__ __forceinline__ void fetch_row(uint4* ring, const T* row, int32_t me, int32_t threads, int32_t C,
-                                          bool vec) {
-  constexpr int U = units_of<T>();
+// Pairs of fp32 values in one 64-bit register: one instruction for two channels.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+constexpr int kPairs = kVec / 2;
+
+// One 8-channel vector as four pairs.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4* u, f2* f) {
+  const T* p = reinterpret_cast<const T*>(u);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int32_t c0 = (me + j * threads) * kVec;
-    if (c0 >= C) continue;
-    if (vec) {
+  for (int i = 0; i < kPairs; ++i) f[i] = pair(to_f<T>(p[2 * i]), to_f<T>(p[2 * i + 1]));
+}
+template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4* u, f2* f) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+// Four pairs as one 8-channel vector, each value rounded once.
+template <typename T> __device__ __forceinline__ void pack(const f2* f, uint4* u);
+template <> __device__ __forceinline__ void pack<__nv_bfloat16>(const f2* f, uint4* u) {
+  __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(u);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) p[i] = __float22bfloat162_rn(split(f[i]));
+}
+template <> __device__ __forceinline__ void pack<__half>(const f2* f, uint4* u) {
+  __half2* p = reinterpret_cast<__half2*>(u);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) p[i] = __float22half2_rn(split(f[i]));
+}
+template <> __device__ __forceinline__ void pack<float>(const f2* f, uint4* u) {
+  float2* p = reinterpret_cast<float2*>(u);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) p[i] = split(f[i]);
+}
+
+// 1 / sqrt(v): the hardware's approximation and one Newton step (within an fp32 step or two).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float n = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+  return v > 0x1p-120f && v < 0x1p120f ? n : r;     // the step itself would leave fp32's range
+}
+
+// Which channels thread `me` of `threads` owns. Aligned rows: whole vectors, j of them `threads`
+// vectors apart. Other rows have no 16-byte accesses, so there a thread's channels lie `threads`
+// apart and every access of a warp is one contiguous piece.
+template <bool kAligned>
+struct Own {
+  static constexpr bool vec = kAligned;
+  int32_t me, threads, C;
+  __device__ __forceinline__ int32_t first(int j) const { return (me + j * threads) * kVec; }     // aligned rows
+  __device__ __forceinline__ int32_t one(int j, int i) const {
+    return vec ? first(j) + i : me + (j * kVec + i) * threads;
+  }
+  // some channel of vector j exists (aligned rows: all or none)
+  __device__ __forceinline__ bool any(int j) const { return (vec ? first(j) : me + j * kVec * threads) < C; }
+};
+
+// This thread's share of a row of T into its own ring slots (slot stride: `threads` units).
+template <typename T, int NV, typename O>
+__device__ __forceinline__ void fetch_row(uint4* ring, const T* row, const O& o) {
+  constexpr int U = units_of<T>();
+  if (o.vec) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (o.first(j) >= o.C) continue;
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        cp_async16(ring + (j * U + u) * threads, reinterpret_cast<const uint4*>(row + c0) + u);
-    } else {
+        cp_async16(ring + (j * U + u) * o.threads, reinterpret_cast<const uint4*>(row + o.first(j)) + u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
       uint4 tmp[U];
       T* p = reinterpret_cast<T*>(tmp);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) p[i] = c0 + i < C ? row[c0 + i] : from_f<T>(0.f);
+      for (int i = 0; i < kVec; ++i) p[i] = o.one(j, i) < o.C ? row[o.one(j, i)] : from_f<T>(0.f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) ring[(j * U + u) * threads] = tmp[u];
+      for (int u = 0; u < U; ++u) ring[(j * U + u) * o.threads] = tmp[u];
     }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void read_vec(const uint4* ring, int j, int32_t threads, float* f) {
+// Vector j of a ring row (zeros where the thread owns nothing).
+template <typename T, typename O>
+__device__ __forceinline__ void read_vec(const uint4* ring, int j, const O& o, f2* f) {
   constexpr int U = units_of<T>();
-  uint4 tmp[U];
+  if (o.any(j)) {
+    uint4 tmp[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) tmp[u] = ring[(j * U + u) * threads];
-  unpack<T>(tmp, f);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int32_t c0, int32_t C, bool vec, const float* f) {
-  constexpr int U = units_of<T>();
-  uint4 tmp[U];
-  T* p = reinterpret_cast<T*>(tmp);
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) p[i] = from_f<T>(f[i]);
-  if (vec) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) reinterpret_cast<uint4*>(row + c0)[u] = tmp[u];
+    for (int u = 0; u < U; ++u) tmp[u] = ring[(j * U + u) * o.threads];
+    unpack<T>(tmp, f);
   } else {
-    for (int i = 0; i < kVec && c0 + i < C; ++i) row[c0 + i] = p[i];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) f[i] = 0ull;
   }
 }
 
+template <typename T, typename O>
+__device__ __forceinline__ void store_vec(T* row, int j, const O& o, const f2* f) {
+  constexpr int U = units_of<T>();
+  uint4 tmp[U];
+  pack<T>(f, tmp);
+  const T* p = reinterpret_cast<const T*>(tmp);
+  if (o.vec) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) reinterpret_cast<uint4*>(row + o.first(j))[u] = tmp[u];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (o.one(j, i) < o.C) row[o.one(j, i)] = p[i];
+  }
+}
+
+// A parameter's values of this thread's channels (0 where it owns nothing), in 16-byte loads that
+// are all in flight together where its rows allow.
+template <typename T, int NV, typename O>
+__device__ __forceinline__ void param_values(const T* p, bool vec, const O& o, float (*f)[kVec]) {
+  constexpr int U = units_of<T>();
+  if (vec && o.vec) {
+    uint4 raw[NV][U];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        raw[j][u] = make_uint4(0, 0, 0, 0);
+        if (o.first(j) < o.C) raw[j][u] = __ldg(reinterpret_cast<const uint4*>(p + o.first(j)) + u);
+      }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const T* t = reinterpret_cast<const T*>(raw[j]);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) f[j][i] = to_f<T>(t[i]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) f[j][i] = o.one(j, i) < o.C ? to_f<T>(p[o.one(j, i)]) : 0.f;
+  }
+}
+template <int NV, typename O>
+__device__ __forceinline__ void load_params(const Param& q, int32_t b, const O& o, float (*f)[kVec]) {
+  if (q.dtype == kBf16)
+    param_values<__nv_bfloat16, NV>(static_cast<const __nv_bfloat16*>(q.p) + b * q.bs, q.vec != 0, o, f);
+  else if (q.dtype == kFp16)
+    param_values<__half, NV>(static_cast<const __half*>(q.p) + b * q.bs, q.vec != 0, o, f);
+  else
+    param_values<float, NV>(static_cast<const float*>(q.p) + b * q.bs, q.vec != 0, o, f);
+}
+
 // Sum of V values over the group. Warp groups: butterflies, every lane gets the sum in the same
-// order. CTA groups: one butterfly, one shared row per warp, one barrier; `buf` alternates so
-// that a slow warp's reads are separated from the next writes by a barrier.
+// order. CTA groups: one butterfly, one shared value per warp, one barrier; `buf` (zero past the
+// last warp) alternates so that a slow warp's reads are separated from the next writes by a
+// barrier.
+constexpr int kMaxWarps = kMaxThreads / 32;
 template <bool kWarp, int V>
-__device__ __forceinline__ void group_sum(float (&v)[V], float (*buf)[V], int32_t warps) {
+__device__ __forceinline__ void group_sum(float (&v)[V], float (*buf)[kMaxWarps]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -168,14 +290,24 @@ __device__ __forceinline__ void group_sum(float (&v)[V], float (*buf)[V], int32_
   if (kWarp) return;
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) buf[threadIdx.x >> 5][i] = v[i];
+    for (int i = 0; i < V; ++i) buf[i][threadIdx.x >> 5] = v[i];
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = 0.f;
-  for (int32_t w = 0; w < warps; ++w)
+  for (int i = 0; i < V; ++i) {
+    float4 q[kMaxWarps / 4];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += buf[w][i];
+    for (int w = 0; w < kMaxWarps / 4; ++w) q[w] = reinterpret_cast<const float4*>(buf[i])[w];
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kMaxWarps / 4; ++w) {
+      t.x += q[w].x;
+      t.y += q[w].y;
+      t.z += q[w].z;
+      t.w += q[w].w;
+    }
+    v[i] = (t.x + t.y) + (t.z + t.w);
+  }
 }
 
 struct Slice { int32_t b, lo, hi; };
@@ -189,141 +321,170 @@ __device__ __forceinline__ Slice slice_of(const Args& a) {
 }
 
 // ------------------------------------------------------------------------------------
-// Forward. TI: type of x; TO: type of y and of the residual.
+// Forward. TI: type of x; TO: type of y and of the residual. 64 registers, so that two CTAs of
+// 512 threads (three of 320) share an SM and one's barriers hide behind the other's work.
 // ------------------------------------------------------------------------------------
-template <typename TI, typename TO, int NV, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads) norm_fwd_kernel(const __grid_constant__ Args a) {
+template <typename TI, typename TO, int NV, bool kWarp, bool kAligned>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads, 2)
+norm_fwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
-  __shared__ float red[2][kMaxThreads / 32][1];
+  __shared__ __align__(16) float red[2][1][kMaxWarps];
   constexpr int UI = units_of<TI>(), UO = units_of<TO>();
   const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
-  const int32_t me = kWarp ? (threadIdx.x & 31) : threadIdx.x;
-  const int32_t warps = threads / 32;
+  const Own<kAligned> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
   const bool has_res = a.res != nullptr;
-  const int stage_units = NV * (UI + (has_res ? UO : 0));
-  uint4* ring = ring_base + (kWarp ? (threadIdx.x >> 5) * a.stages * stage_units * 32 : 0) + me;
+  const int stage_units = NV * (UI + (has_res ? UO : 0)) * threads;
+  uint4* ring = ring_base + (kWarp ? (threadIdx.x >> 5) * a.stages * stage_units : 0) + o.me;
   const Slice s = slice_of(a);
   const int32_t step = kWarp ? kWarpsPerCta : 1;
   const int32_t first = s.lo + (kWarp ? static_cast<int32_t>(threadIdx.x >> 5) : 0);
   const TI* x = static_cast<const TI*>(a.x) + s.b * a.xb;
   const TO* res = has_res ? static_cast<const TO*>(a.res) + s.b * a.rb : nullptr;
   TO* y = static_cast<TO*>(a.y) + s.b * a.yb;
-  const bool vec = a.vec != 0;
+  if (!kWarp && threadIdx.x < 2 * kMaxWarps) (&red[0][0][0])[threadIdx.x] = 0.f;
 
-  auto fetch = [&](int32_t row, int st) {
-    if (row < s.hi) {
-      uint4* slot = ring + st * stage_units * threads;
-      fetch_row<TI, NV>(slot, x + row * a.xn, me, threads, a.C, vec);
-      if (has_res) fetch_row<TO, NV>(slot + NV * UI * threads, res + row * a.rn, me, threads, a.C, vec);
+  // rows are fetched one after the other: the next one's addresses
+  x += first * a.xn;
+  if (has_res) res += first * a.rn;
+  y += first * a.yn;
+  const int64_t xstep = step * a.xn, rstep = step * a.rn, ystep = step * a.yn;
+  int32_t next = first;
+  auto fetch = [&](uint4* slot) {
+    if (next < s.hi) {
+      fetch_row<TI, NV>(slot, x, o);
+      if (has_res) fetch_row<TO, NV>(slot + NV * UI * threads, res, o);
     }
     cp_async_commit();
+    x += xstep;
+    res += rstep;
+    next += step;
   };
   const int32_t stages = a.stages;
-  for (int i = 0; i < stages - 1; ++i) fetch(first + i * step, i);
+  uint4* const ring_end = ring + stages * stage_units;
+  uint4* free_slot = ring;
+  for (int i = 0; i < stages - 1; ++i, free_slot += stage_units) fetch(free_slot);
 
   // A and S of this thread's channels
-  float A[NV][kVec], S[NV][kVec];
+  f2 A[NV][kPairs], S[NV][kPairs];
+  {
+    float g[NV][kVec], w[NV][kVec], sh[NV][kVec];
+    if (a.g.p) load_params<NV>(a.g, s.b, o, g);
+    if (a.w.p) load_params<NV>(a.w, 0, o, w);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int32_t c = (me + j * threads) * kVec + i;
-      float w = 0.f, sh = 0.f;
-      if (c < a.C) {
-        const float gain = a.g.p ? a.gain_off + load_param(a.g, s.b, c) : 1.f;
-        w = a.w.p ? gain * load_param(a.w, 0, c) : gain;
-        sh = a.t.p ? load_param(a.t, s.b, c) : 0.f;
-        if (a.b.p) sh = fmaf(gain, load_param(a.b, 0, c), sh);
+      for (int i = 0; i < kVec; ++i) {
+        g[j][i] = a.g.p ? a.gain_off + g[j][i] : 1.f;
+        w[j][i] = a.w.p ? g[j][i] * w[j][i] : g[j][i];
+        sh[j][i] = 0.f;
       }
-      A[j][i] = w;
-      S[j][i] = sh;
-    }
-  }
-
-  int st = 0;
-  int32_t flip = 0;
-  for (int32_t row = first; row < s.hi; row += step) {
-    wait_oldest(stages);
-    const uint4* slot = ring + st * stage_units * threads;
-    float v[NV][kVec];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int32_t c0 = (me + j * threads) * kVec;
-      if (c0 < a.C) {
-        read_vec<TI>(slot, j, threads, v[j]);
-      } else {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[j][i] = 0.f;
-      }
-    }
-    // the row that will use the slot read in the previous round
-    fetch(row + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);
-    float mean = 0.f, rstd = 1.f;
-    if (a.kind == kLayer) {
-      float m[1] = {0.f};
+      for (int i = 0; i < kPairs; ++i) A[j][i] = pair(w[j][2 * i], w[j][2 * i + 1]);
+    if (a.t.p) load_params<NV>(a.t, s.b, o, sh);
+    if (a.b.p) {
+      load_params<NV>(a.b, 0, o, w);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) m[0] += v[j][i];
-      group_sum<kWarp, 1>(m, red[flip], warps);
+        for (int i = 0; i < kVec; ++i) sh[j][i] = fmaf(g[j][i], w[j][i], sh[j][i]);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) S[j][i] = pair(sh[j][2 * i], sh[j][2 * i + 1]);
+  }
+  if (!kWarp) __syncthreads();                     // red is zero
+
+  uint4* slot = ring;
+  int32_t flip = 0;
+  for (int32_t row = first; row < s.hi; row += step) {
+    wait_oldest(stages);
+    f2 v[NV][kPairs];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) read_vec<TI>(slot, j, o, v[j]);
+    fetch(free_slot);                              // the slot read in the previous round
+    float mean = 0.f, rstd = 1.f;
+    if (a.kind == kLayer) {
+      f2 t = 0ull;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) t = add2(t, v[j][i]);
+      float m[1] = {split(t).x + split(t).y};
+      group_sum<kWarp, 1>(m, red[flip]);
       flip ^= 1;
       mean = m[0] * a.inv_c;
-    }
-    if (a.kind != kNone) {
-      float q[1] = {0.f};
+      const f2 sub = pair(-mean, -mean);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int32_t c0 = (me + j * threads) * kVec;
+        if (!o.any(j)) continue;                   // what the thread does not own stays 0
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          v[j][i] = c0 + i < a.C ? v[j][i] - mean : 0.f;
-          q[0] = fmaf(v[j][i], v[j][i], q[0]);
+        for (int i = 0; i < kPairs; ++i) v[j][i] = add2(v[j][i], sub);
+        if (!o.vec) {
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            const float2 q = split(v[j][i]);
+            v[j][i] = pair(o.one(j, 2 * i) < a.C ? q.x : 0.f, o.one(j, 2 * i + 1) < a.C ? q.y : 0.f);
+          }
         }
       }
-      group_sum<kWarp, 1>(q, red[flip], warps);
-      flip ^= 1;
-      rstd = 1.0f / sqrtf(fmaf(q[0], a.inv_c, a.eps));
     }
-    if (a.rstd != nullptr && me == 0) {
+    if (a.kind != kNone) {
+      f2 t = 0ull;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) t = fma2(v[j][i], v[j][i], t);
+      float q[1] = {split(t).x + split(t).y};
+      group_sum<kWarp, 1>(q, red[flip]);
+      flip ^= 1;
+      rstd = inv_sqrt(fmaf(q[0], a.inv_c, a.eps));
+    }
+    if (a.rstd != nullptr && o.me == 0) {
       const int64_t r = static_cast<int64_t>(s.b) * a.N + row;
       if (a.mean != nullptr) a.mean[r] = mean;
       a.rstd[r] = rstd;
     }
-    TO* out = y + row * a.yn;
+    const f2 rs = pair(rstd, rstd), scale = pair(a.res_scale, a.res_scale);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int32_t c0 = (me + j * threads) * kVec;
-      if (c0 >= a.C) continue;
-      float o[kVec];
+      if (!o.any(j)) continue;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) o[i] = fmaf(v[j][i] * rstd, A[j][i], S[j][i]);
+      for (int i = 0; i < kPairs; ++i) v[j][i] = fma2(mul2(v[j][i], rs), A[j][i], S[j][i]);
       if (has_res) {
-        float r[kVec];
-        read_vec<TO>(slot + NV * UI * threads, j, threads, r);
+        f2 r[kPairs];
+        read_vec<TO>(slot + NV * UI * threads, j, o, r);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) o[i] = fmaf(r[i], a.res_scale, o[i]);
+        for (int i = 0; i < kPairs; ++i) v[j][i] = fma2(r[i], scale, v[j][i]);
       }
-      store_vec<TO>(out, c0, a.C, vec, o);
+      store_vec<TO>(y, j, o, v[j]);
     }
-    st = st == stages - 1 ? 0 : st + 1;
+    y += ystep;
+    free_slot = slot;
+    slot = slot + stage_units == ring_end ? ring : slot + stage_units;
   }
   cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------------------------
-// Backward. TI: type of x, dx and of the gradient around the block; TO: type of dy.
+// Backward. TI: type of x, dx and of the gradient around the block; TO: type of dy. A, P1 and P2
+// take 24 registers a vector; xh and g are therefore formed twice, before and after the row's
+// sums, from the ring (whose slot is not refilled before the next row) instead of being held.
+// kBound: most threads of the CTA; 320 (up to 5,120 channels) leaves room for two CTAs an SM.
 // ------------------------------------------------------------------------------------
-template <typename TI, typename TO, int NV, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads) norm_bwd_kernel(const __grid_constant__ Args a) {
+template <typename TI, typename TO, int NV, bool kWarp, int kBound, bool kAligned>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kBound, kBound == kMaxThreads || (kWarp && NV == 4) ? 1 : 2)
+norm_bwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
-  __shared__ float red[2][kMaxThreads / 32][2];
+  __shared__ __align__(16) float red[2][2][kMaxWarps];
   constexpr int UI = units_of<TI>(), UO = units_of<TO>();
   const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
-  const int32_t me = kWarp ? (threadIdx.x & 31) : threadIdx.x;
-  const int32_t warps = threads / 32;
+  const Own<kAligned> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
   const bool has_res = a.res != nullptr;
-  const int stage_units = NV * (UI + UO + (has_res ? UI : 0));
-  uint4* ring = ring_base + (kWarp ? (threadIdx.x >> 5) * a.stages * stage_units * 32 : 0) + me;
+  const int stage_units = NV * (UI + UO + (has_res ? UI : 0)) * threads;
+  uint4* ring = ring_base + (kWarp ? (threadIdx.x >> 5) * a.stages * stage_units : 0) + o.me;
   const Slice s = slice_of(a);
   const int32_t step = kWarp ? kWarpsPerCta : 1;
   const int32_t first = s.lo + (kWarp ? static_cast<int32_t>(threadIdx.x >> 5) : 0);
@@ -331,92 +492,113 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads) norm_
   const TO* dy = static_cast<const TO*>(a.dy) + s.b * a.db;
   const TI* res = has_res ? static_cast<const TI*>(a.res) + s.b * a.rb : nullptr;
   TI* dx = static_cast<TI*>(a.y) + s.b * a.yb;
-  const bool vec = a.vec != 0;
+  if (!kWarp && threadIdx.x < 4 * kMaxWarps) (&red[0][0][0])[threadIdx.x] = 0.f;
 
-  auto fetch = [&](int32_t row, int st) {
-    if (row < s.hi) {
-      uint4* slot = ring + st * stage_units * threads;
-      fetch_row<TI, NV>(slot, x + row * a.xn, me, threads, a.C, vec);
-      fetch_row<TO, NV>(slot + NV * UI * threads, dy + row * a.dn, me, threads, a.C, vec);
-      if (has_res)
-        fetch_row<TI, NV>(slot + NV * (UI + UO) * threads, res + row * a.rn, me, threads, a.C, vec);
+  // rows are fetched one after the other: the next one's addresses
+  x += first * a.xn;
+  dy += first * a.dn;
+  if (has_res) res += first * a.rn;
+  dx += first * a.yn;
+  const int64_t xstep = step * a.xn, dstep = step * a.dn, rstep = step * a.rn, ystep = step * a.yn;
+  int32_t next = first;
+  auto fetch = [&](uint4* slot) {
+    if (next < s.hi) {
+      fetch_row<TI, NV>(slot, x, o);
+      fetch_row<TO, NV>(slot + NV * UI * threads, dy, o);
+      if (has_res) fetch_row<TI, NV>(slot + NV * (UI + UO) * threads, res, o);
     }
     cp_async_commit();
+    x += xstep;
+    dy += dstep;
+    res += rstep;
+    next += step;
   };
   const int32_t stages = a.stages;
-  for (int i = 0; i < stages - 1; ++i) fetch(first + i * step, i);
+  uint4* const ring_end = ring + stages * stage_units;
+  uint4* free_slot = ring;
+  for (int i = 0; i < stages - 1; ++i, free_slot += stage_units) fetch(free_slot);
 
-  float A[NV][kVec], P1[NV][kVec], P2[NV][kVec];
+  f2 A[NV][kPairs], P1[NV][kPairs], P2[NV][kPairs];
+  {
+    float g[NV][kVec], w[NV][kVec];
+    if (a.g.p) load_params<NV>(a.g, s.b, o, g);
+    if (a.w.p) load_params<NV>(a.w, 0, o, w);
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int32_t c = (me + j * threads) * kVec + i;
-      float w = 0.f;
-      if (c < a.C) {
-        w = a.g.p ? a.gain_off + load_param(a.g, s.b, c) : 1.f;
-        if (a.w.p) w *= load_param(a.w, 0, c);
-      }
-      A[j][i] = w;
-      P1[j][i] = P2[j][i] = 0.f;
-    }
-  }
-
-  int st = 0;
-  int32_t flip = 0;
-  for (int32_t row = first; row < s.hi; row += step) {
-    const int64_t r = static_cast<int64_t>(s.b) * a.N + row;
-    const float mean = a.kind == kLayer ? __ldg(a.mean + r) : 0.f;
-    const float rstd = a.kind != kNone ? __ldg(a.rstd + r) : 1.f;
-    wait_oldest(stages);
-    const uint4* slot = ring + st * stage_units * threads;
-    float xh[NV][kVec], g[NV][kVec];
-    float sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int32_t c0 = (me + j * threads) * kVec;
-      if (c0 < a.C) {
-        read_vec<TI>(slot, j, threads, xh[j]);
-        read_vec<TO>(slot + NV * UI * threads, j, threads, g[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) xh[j][i] = g[j][i] = 0.f;
-      }
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        xh[j][i] = (xh[j][i] - mean) * rstd;
-        P1[j][i] = fmaf(g[j][i], xh[j][i], P1[j][i]);
-        P2[j][i] += g[j][i];
-        g[j][i] *= A[j][i];                       // 0 past the last channel
-        sum[0] += g[j][i];
-        sum[1] = fmaf(g[j][i], xh[j][i], sum[1]);
+        g[j][i] = a.g.p ? a.gain_off + g[j][i] : 1.f;
+        if (a.w.p) g[j][i] *= w[j][i];
       }
-    }
-    fetch(row + (stages - 1) * step, st == 0 ? stages - 1 : st - 1);
-    float c1 = 0.f, c2 = 0.f;
-    if (a.kind != kNone) {
-      group_sum<kWarp, 2>(sum, red[flip], warps);
-      flip ^= 1;
-      c1 = a.kind == kLayer ? sum[0] * a.inv_c : 0.f;
-      c2 = sum[1] * a.inv_c;
-    }
-    TI* out = dx + row * a.yn;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        A[j][i] = pair(g[j][2 * i], g[j][2 * i + 1]);
+        P1[j][i] = P2[j][i] = 0ull;
+      }
+  }
+  if (!kWarp) __syncthreads();                     // red is zero
+
+  uint4* slot = ring;
+  int32_t flip = 0;
+  const float* means = a.mean + static_cast<int64_t>(s.b) * a.N;
+  const float* rstds = a.rstd + static_cast<int64_t>(s.b) * a.N;
+  for (int32_t row = first; row < s.hi; row += step) {
+    const float mean = a.kind == kLayer ? __ldg(means + row) : 0.f;
+    const float rstd = a.kind != kNone ? __ldg(rstds + row) : 1.f;
+    wait_oldest(stages);
+    const f2 sub = pair(-mean, -mean), rs = pair(rstd, rstd);
+    // xh of vector j: 0 where the thread owns nothing is not needed, dy is 0 there
+    auto normed = [&](int j, f2* xh) {
+      read_vec<TI>(slot, j, o, xh);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) xh[i] = mul2(add2(xh[i], sub), rs);
+    };
+    f2 t1 = 0ull, t2 = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int32_t c0 = (me + j * threads) * kVec;
-      if (c0 >= a.C) continue;
-      float o[kVec];
+      f2 xh[kPairs], g[kPairs];
+      normed(j, xh);
+      read_vec<TO>(slot + NV * UI * threads, j, o, g);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) o[i] = (fmaf(-xh[j][i], c2, g[j][i]) - c1) * rstd;
-      if (has_res) {
-        float q[kVec];
-        read_vec<TI>(slot + NV * (UI + UO) * threads, j, threads, q);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) o[i] = fmaf(q[i], a.res_scale, o[i]);
+      for (int i = 0; i < kPairs; ++i) {
+        P1[j][i] = fma2(g[i], xh[i], P1[j][i]);
+        P2[j][i] = add2(P2[j][i], g[i]);
+        const f2 q = mul2(g[i], A[j][i]);
+        t1 = add2(t1, q);
+        t2 = fma2(q, xh[i], t2);
       }
-      store_vec<TI>(out, c0, a.C, vec, o);
     }
-    st = st == stages - 1 ? 0 : st + 1;
+    fetch(free_slot);                              // the slot read in the previous round
+    float c1 = 0.f, c2 = 0.f;
+    if (a.kind != kNone) {
+      float sum[2] = {split(t1).x + split(t1).y, split(t2).x + split(t2).y};
+      group_sum<kWarp, 2>(sum, red[flip]);
+      flip ^= 1;
+      c1 = a.kind == kLayer ? -sum[0] * a.inv_c : 0.f;
+      c2 = -sum[1] * a.inv_c;
+    }
+    const f2 k1 = pair(c1, c1), k2 = pair(c2, c2), scale = pair(a.res_scale, a.res_scale);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (!o.any(j)) continue;
+      f2 xh[kPairs], g[kPairs];
+      normed(j, xh);
+      read_vec<TO>(slot + NV * UI * threads, j, o, g);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) g[i] = mul2(add2(fma2(xh[i], k2, mul2(g[i], A[j][i])), k1), rs);
+      if (has_res) {
+        f2 q[kPairs];
+        read_vec<TI>(slot + NV * (UI + UO) * threads, j, o, q);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) g[i] = fma2(q[i], scale, g[i]);
+      }
+      store_vec<TI>(dx, j, o, g);
+    }
+    dx += ystep;
+    free_slot = slot;
+    slot = slot + stage_units == ring_end ? ring : slot + stage_units;
   }
   cp_async_wait<0>();
 
@@ -424,16 +606,15 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads) norm_
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.C;
   if (!kWarp) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const int32_t c = (me + j * threads) * kVec + i;
-        if (c < a.C) {
-          part[c] = P1[j][i];
-          part[a.C + c] = P2[j][i];
-        }
+        const int32_t c = o.one(j, i);
+        if (c >= a.C) continue;
+        const float2 q1 = split(P1[j][i / 2]), q2 = split(P2[j][i / 2]);
+        part[c] = i % 2 ? q1.y : q1.x;
+        part[a.C + c] = i % 2 ? q2.y : q2.x;
       }
-    }
     return;
   }
   float* acc = reinterpret_cast<float*>(ring_base);      // [2][NV * 256]: the ring is drained
@@ -442,14 +623,15 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads) norm_
     __syncthreads();
     if (static_cast<int32_t>(threadIdx.x >> 5) != w) continue;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const int32_t c = (me + j * 32) * kVec + i;
-        acc[c] = w ? acc[c] + P1[j][i] : P1[j][i];
-        acc[W + c] = w ? acc[W + c] + P2[j][i] : P2[j][i];
+        const int32_t c = o.one(j, i);                   // < W for both mappings
+        const float2 q1 = split(P1[j][i / 2]), q2 = split(P2[j][i / 2]);
+        const float p1 = i % 2 ? q1.y : q1.x, p2 = i % 2 ? q2.y : q2.x;
+        acc[c] = w ? acc[c] + p1 : p1;
+        acc[W + c] = w ? acc[W + c] + p2 : p2;
       }
-    }
   }
   __syncthreads();
   for (int32_t c = threadIdx.x; c < a.C; c += 32 * kWarpsPerCta) {
@@ -459,7 +641,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads) norm_
 }
 
 // ------------------------------------------------------------------------------------
-// Parameter gradients from the slices' sums. One CTA per 32 channels and sequence: 8 rows of
+// Parameter gradients from the slices' sums. One CTA per 32 channels and sequence: 16 rows of
 // threads add up the slices (a fixed assignment and order), then
 //   dG = w P1 + b P2, dshift = P2, and the sequence's G P1, G P2 for dw, db.
 // ------------------------------------------------------------------------------------
@@ -469,10 +651,12 @@ struct GradArgs {
   float gain_off;
   float* dgain;            // null or [B][C]
   float* dshift;           // null or [B][C]
-  float* gp;               // [B][2][C]: G P1, G P2 (null when neither dw nor db is asked for)
+  float* gp;               // [B][2][C]: G P1, G P2 for norm_weight_grad_kernel, or null
+  float* dw;               // one sequence: [C] or null
+  float* db;
   int32_t B, C, slices;
 };
-constexpr int kGradRows = 8;
+constexpr int kGradRows = 16;
 
 __global__ void __launch_bounds__(32 * kGradRows) norm_grad_kernel(const __grid_constant__ GradArgs a) {
   __shared__ float s1[kGradRows][32], s2[kGradRows][32];
@@ -481,7 +665,7 @@ __global__ void __launch_bounds__(32 * kGradRows) norm_grad_kernel(const __grid_
   float p1 = 0.f, p2 = 0.f;
   if (c < a.C) {
     const float* part = a.part + static_cast<int64_t>(b) * a.slices * 2 * a.C + c;
-#pragma unroll 4
+#pragma unroll 8
     for (int32_t i = r; i < a.slices; i += kGradRows) {
       p1 += part[static_cast<int64_t>(i) * 2 * a.C];
       p2 += part[static_cast<int64_t>(i) * 2 * a.C + a.C];
@@ -502,8 +686,10 @@ __global__ void __launch_bounds__(32 * kGradRows) norm_grad_kernel(const __grid_
     a.dgain[o] = a.b.p ? fmaf(w, p1, load_param(a.b, 0, c) * p2) : w * p1;
   }
   if (a.dshift) a.dshift[o] = p2;
+  const float G = a.g.p ? a.gain_off + load_param(a.g, b, c) : 1.f;
+  if (a.dw) a.dw[c] = G * p1;
+  if (a.db) a.db[c] = G * p2;
   if (a.gp) {
-    const float G = a.g.p ? a.gain_off + load_param(a.g, b, c) : 1.f;
     a.gp[static_cast<int64_t>(b) * 2 * a.C + c] = G * p1;
     a.gp[static_cast<int64_t>(b) * 2 * a.C + a.C + c] = G * p2;
   }

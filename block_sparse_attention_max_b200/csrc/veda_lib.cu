@@ -269,6 +269,15 @@ veda_status host_device(int& sms) { return current_device(sms); }
 using namespace veda;
 
 namespace {
+veda_status check_int8_product(const char* call, const void* a, const float* a_scale, const void* w, const float* w_scale,
+                               const float* bias, const void* y, int64_t y_stride, int32_t dtype, int32_t M, int32_t N) {
+  if (!a || !a_scale || !w || !w_scale || !y || !aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) ||
+      !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(y, type_size(dtype)))
+    return fail(VEDA_ERR_INVALID_ARG, std::string(call) + ": missing or misaligned buffer");
+  if (M > 1 && y_stride < N) return fail(VEDA_ERR_INVALID_ARG, std::string(call) + ": rows of y overlap");
+  return VEDA_OK;
+}
+
 template <typename T>
 veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
   if (p.M <= int8::kFewMax) {
@@ -1024,13 +1033,10 @@ veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w,
     if (K > 131071) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_matmul: K above 131071 overflows the integer sum");
     if (M == 0 || N == 0) return VEDA_OK;
     const int64_t es = type_size(dtype);
-    if (!a || !a_scale || !w || !w_scale || !y || !aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) ||
-        !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(y, es))
-      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_matmul: missing or misaligned buffer");
-    if (M > 1 && y_stride < N) return fail(VEDA_ERR_INVALID_ARG, "veda_int8_matmul: rows of y overlap");
-    int sms;
-    veda_status st = current_device(sms);
+    veda_status st = check_int8_product("veda_int8_matmul", a, a_scale, w, w_scale, bias, y, y_stride, dtype, M, N);
     if (st != VEDA_OK) return st;
+    int sms;
+    if ((st = current_device(sms)) != VEDA_OK) return st;
     int8::MatArgs p{};
     p.a = static_cast<const int8_t*>(a); p.w = static_cast<const int8_t*>(w);
     p.sa = a_scale; p.sw = w_scale; p.bias = bias;
@@ -1044,6 +1050,31 @@ veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w,
     if (dtype == VEDA_BF16) return launch_int8<__nv_bfloat16>(p, sms, s);
     if (dtype == VEDA_FP16) return launch_int8<__half>(p, sms, s);
     return launch_int8<float>(p, sms, s);
+  });
+}
+
+size_t veda_int8_linear_workspace_bytes(int32_t M, int32_t K) {
+  if (M <= 0 || K <= 0 || K > 131071) return 0;
+  const size_t kp = (static_cast<size_t>(K) + 15) / 16 * 16;
+  return static_cast<size_t>(M) * kp + static_cast<size_t>(M) * sizeof(float);
+}
+
+veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, const void* w, const float* w_scale,
+                             const float* bias, void* y, int64_t y_stride, int32_t y_dtype, void* workspace,
+                             size_t workspace_bytes, int32_t M, int32_t N, int32_t K, veda_stream_t stream) {
+  return guarded("veda_int8_linear", [&]() -> veda_status {
+    if (M < 0 || N < 0 || K <= 0 || !known_type(x_dtype) || !known_type(y_dtype) || y_stride < 0)
+      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: bad size or type");
+    if (K > 131071) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_linear: K above 131071 overflows the integer sum");
+    if (M == 0 || N == 0) return VEDA_OK;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < veda_int8_linear_workspace_bytes(M, K))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: workspace too small or misaligned");
+    const size_t kp = (static_cast<size_t>(K) + 15) / 16 * 16;
+    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + static_cast<size_t>(M) * kp);
+    veda_status st = check_int8_product("veda_int8_linear", workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N);
+    if (st != VEDA_OK) return st;
+    if ((st = veda_quantize_int8(x, x_stride, x_dtype, workspace, scale, M, K, stream)) != VEDA_OK) return st;
+    return veda_int8_matmul(workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N, K, stream);
   });
 }
 

@@ -5,7 +5,9 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <map>
 #include <mutex>
+#include <tuple>
 
 #include "k_norm.cuh"
 #include "veda_host.h"
@@ -53,11 +55,11 @@ Shape shape_of(int32_t C) {
 typedef void (*Kernel)(const Args);
 
 // The kernels of one shape and type pair; null for a pair that is not built.
-template <int NV, bool W>
+template <int NV, bool W, int BOUND, bool A>
 Kernel pick_types(bool bwd, int32_t ti, int32_t to) {
   using B = __nv_bfloat16;
   using H = __half;
-#define VEDA_PAIR(TI, TO) (bwd ? norm::norm_bwd_kernel<TI, TO, NV, W> : norm::norm_fwd_kernel<TI, TO, NV, W>)
+#define VEDA_PAIR(TI, TO) (bwd ? norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, A> : norm::norm_fwd_kernel<TI, TO, NV, W, A>)
   if (ti == VEDA_BF16 && to == VEDA_BF16) return VEDA_PAIR(B, B);
   if (ti == VEDA_FP16 && to == VEDA_FP16) return VEDA_PAIR(H, H);
   if (ti == VEDA_FP32 && to == VEDA_FP32) return VEDA_PAIR(float, float);
@@ -66,13 +68,19 @@ Kernel pick_types(bool bwd, int32_t ti, int32_t to) {
 #undef VEDA_PAIR
   return nullptr;
 }
-Kernel pick(const Shape& s, bool bwd, int32_t ti, int32_t to) {
+template <bool A>
+Kernel pick_shape(const Shape& s, bool bwd, int32_t ti, int32_t to) {
   if (s.warp) {
-    if (s.nv == 1) return pick_types<1, true>(bwd, ti, to);
-    if (s.nv == 2) return pick_types<2, true>(bwd, ti, to);
-    return pick_types<4, true>(bwd, ti, to);
+    if (s.nv == 1) return pick_types<1, true, 256, A>(bwd, ti, to);
+    if (s.nv == 2) return pick_types<2, true, 256, A>(bwd, ti, to);
+    return pick_types<4, true, 256, A>(bwd, ti, to);
   }
-  return pick_types<2, false>(bwd, ti, to);
+  return s.threads <= 320 ? pick_types<2, false, 320, A>(bwd, ti, to)
+                          : pick_types<2, false, norm::kMaxThreads, A>(bwd, ti, to);
+}
+// aligned: every row starts on a 16-byte boundary and C % 8 == 0
+Kernel pick(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to) {
+  return is_aligned ? pick_shape<true>(s, bwd, ti, to) : pick_shape<false>(s, bwd, ti, to);
 }
 
 // Ring bytes of a CTA: every row a group has in flight, 16-byte units.
@@ -85,28 +93,44 @@ int ring_bytes(const Shape& s, bool bwd, int32_t ti, int32_t to, bool res, int32
   return stages * row;
 }
 
+// CTAs of this kernel that fit an SM, asked once per device, kernel and ring. Rings over the
+// default limit (48 KB with the static part) are opted into first, always with the same maximum,
+// so that calls from two threads cannot take it from one another.
+veda_status resident(Kernel k, int threads, int bytes, int& per_sm) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, Kernel, int, int>, int> known_fits;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(dev, k, threads, bytes);
+  const auto it = known_fits.find(key);
+  if (it != known_fits.end()) {
+    per_sm = it->second;
+    return VEDA_OK;
+  }
+  const void* f = reinterpret_cast<const void*>(k);
+  if (bytes > 32 * 1024 &&
+      (e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing)) != cudaSuccess)
+    return cuda_fail(e, "cudaFuncSetAttribute");
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f, threads, static_cast<size_t>(bytes))) != cudaSuccess)
+    return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  known_fits[key] = per_sm;
+  return VEDA_OK;
+}
+
 // Slices per sequence: together the CTAs that can run at once (so a CTA keeps its channels'
 // parameters for as many rows as possible), no more than there are rows.
 constexpr int kMaxPerSmFwd = 8, kMaxPerSmBwd = 4, kMaxSms = 160;
 veda_status slices_for(Kernel k, const Shape& s, int bytes, int sms, int cap, int32_t B, int32_t N, int32_t& slices) {
   int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(k),
-                                                                      s.threads, static_cast<size_t>(bytes));
-  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+  const veda_status st = resident(k, s.threads, bytes, per_sm);
+  if (st != VEDA_OK) return st;
   per_sm = std::max(1, std::min(per_sm, cap));
   const int64_t want = (static_cast<int64_t>(std::min(sms, kMaxSms)) * per_sm + B - 1) / B;
   const int64_t rows = s.warp ? (N + norm::kWarpsPerCta - 1) / norm::kWarpsPerCta : N;
   slices = static_cast<int32_t>(std::max<int64_t>(1, std::min(want, rows)));
   return VEDA_OK;
-}
-
-// Rings over the default limit (48 KB with the static part) need an opt-in; always the same one,
-// so that calls from two threads cannot take it from one another.
-veda_status allow_smem(Kernel k, int bytes) {
-  if (bytes <= 32 * 1024) return VEDA_OK;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
-  return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "cudaFuncSetAttribute");
 }
 
 veda_status check_common(const char* call, int32_t x_dtype, int32_t y_dtype, const veda_norm_params* q, int32_t B,
@@ -118,7 +142,7 @@ veda_status check_common(const char* call, int32_t x_dtype, int32_t y_dtype, con
   if (kind < VEDA_NORM_LAYER || kind > VEDA_NORM_NONE) return fail(VEDA_ERR_INVALID_ARG, c + ": unknown kind of norm");
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(VEDA_ERR_INVALID_ARG, c + ": eps must be finite and >= 0");
   if (C > norm::kMaxCols) return fail(VEDA_ERR_UNSUPPORTED, c + ": more than 8192 channels");
-  if (!pick({1, true, 0}, false, x_dtype, y_dtype))
+  if (!pick({1, true, 0}, false, true, x_dtype, y_dtype))
     return fail(VEDA_ERR_UNSUPPORTED, c + ": input and output types must be equal, or bf16 and fp32");
   const int64_t ws = size_of(q->weight_dtype), ms = size_of(q->mod_dtype);
   if (!on(q->weight, ws) || !on(q->bias, ws) || !on(q->gain, ms) || !on(q->shift, ms))
@@ -127,10 +151,13 @@ veda_status check_common(const char* call, int32_t x_dtype, int32_t y_dtype, con
 }
 
 void set_params(Args& a, const veda_norm_params* q) {
-  a.w = {q->weight, 0, q->weight_dtype};
-  a.b = {q->bias, 0, q->weight_dtype};
-  a.g = {q->gain, q->gain_stride, q->mod_dtype};
-  a.t = {q->shift, q->shift_stride, q->mod_dtype};
+  const auto param = [&](const void* p, int64_t stride, int32_t dtype) {
+    return norm::Param{p, stride, dtype, a.C % norm::kVec == 0 && vec_rows(p, stride, 0, dtype) ? 1 : 0};
+  };
+  a.w = param(q->weight, 0, q->weight_dtype);
+  a.b = param(q->bias, 0, q->weight_dtype);
+  a.g = param(q->gain, q->gain_stride, q->mod_dtype);
+  a.t = param(q->shift, q->shift_stride, q->mod_dtype);
   a.gain_off = q->gain_offset;
 }
 
@@ -163,16 +190,16 @@ veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const v
     a.x = x->data; a.xb = x->batch_stride; a.xn = x->row_stride;
     a.y = y->data; a.yb = y->batch_stride; a.yn = y->row_stride;
     if (residual) { a.res = residual->data; a.rb = residual->batch_stride; a.rn = residual->row_stride; }
+    a.C = C;
     set_params(a, params);
     a.res_scale = residual_scale; a.eps = eps; a.inv_c = 1.0f / static_cast<float>(C);
     a.mean = mean; a.rstd = rstd;
-    a.B = B; a.N = N; a.C = C; a.kind = kind;
-    a.vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.y, a.yb, a.yn, y->dtype) &&
+    a.B = B; a.N = N; a.kind = kind;
+    const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.y, a.yb, a.yn, y->dtype) &&
             (!residual || vec_rows(a.res, a.rb, a.rn, y->dtype));
     const Shape s = shape_of(C);
     const int bytes = ring_bytes(s, false, x->dtype, y->dtype, residual != nullptr, a.stages);
-    const Kernel k = pick(s, false, x->dtype, y->dtype);
-    if ((st = allow_smem(k, bytes)) != VEDA_OK) return st;
+    const Kernel k = pick(s, false, vec, x->dtype, y->dtype);
     if ((st = slices_for(k, s, bytes, sms, kMaxPerSmFwd, B, N, a.slices)) != VEDA_OK) return st;
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
@@ -229,17 +256,17 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     a.dy = dy->data; a.db = dy->batch_stride; a.dn = dy->row_stride;
     a.y = dx->data; a.yb = dx->batch_stride; a.yn = dx->row_stride;
     if (residual_grad) { a.res = residual_grad->data; a.rb = residual_grad->batch_stride; a.rn = residual_grad->row_stride; }
+    a.C = C;
     set_params(a, params);
     a.res_scale = residual_scale; a.inv_c = 1.0f / static_cast<float>(C);
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
-    a.B = B; a.N = N; a.C = C; a.kind = kind;
-    a.vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.dy, a.db, a.dn, dy->dtype) &&
+    a.B = B; a.N = N; a.kind = kind;
+    const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.dy, a.db, a.dn, dy->dtype) &&
             vec_rows(a.y, a.yb, a.yn, x->dtype) && (!a.res || vec_rows(a.res, a.rb, a.rn, x->dtype));
     const Shape s = shape_of(C);
     const int bytes = ring_bytes(s, true, x->dtype, dy->dtype, a.res != nullptr, a.stages);
     a.part = static_cast<float*>(workspace);
-    const Kernel k = pick(s, true, x->dtype, dy->dtype);
-    if ((st = allow_smem(k, bytes)) != VEDA_OK) return st;
+    const Kernel k = pick(s, true, vec, x->dtype, dy->dtype);
     if ((st = slices_for(k, s, bytes, sms, kMaxPerSmBwd, B, N, a.slices)) != VEDA_OK) return st;
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, s0>>>(a);
     cudaError_t e = cudaGetLastError();
@@ -251,7 +278,11 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     g.gain_off = a.gain_off;
     g.dgain = dgain; g.dshift = dshift;
     g.B = B; g.C = C; g.slices = a.slices;
-    g.gp = dweight || dbias ? a.part + static_cast<int64_t>(B) * a.slices * 2 * C : nullptr;
+    if (B == 1) {
+      g.dw = dweight; g.db = dbias;
+    } else if (dweight || dbias) {
+      g.gp = a.part + static_cast<int64_t>(B) * a.slices * 2 * C;
+    }
     norm::norm_grad_kernel<<<dim3((C + 31) / 32, B), 32 * norm::kGradRows, 0, s0>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "norm_grad_kernel");
     if (g.gp) {

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -33,7 +34,7 @@ EXPORTED = (
     "veda_quantize_fp8", "veda_block_sparse_attn_fwd_fp8",
     "veda_rotary_table", "veda_rotary", "veda_rotary_permute_pool", "veda_rotary_unpermute",
     "veda_norm_fwd", "veda_norm_bwd_workspace_bytes", "veda_norm_bwd",
-    "veda_quantize_int8", "veda_int8_matmul",
+    "veda_quantize_int8", "veda_int8_matmul", "veda_int8_linear_workspace_bytes", "veda_int8_linear",
     "veda_check_device_status", "veda_selftest_wait_timeout",
 )
 
@@ -56,16 +57,10 @@ class Geometry(ctypes.Structure):
                 ("order_stride", ctypes.c_int32)]
 
 
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
-                ("dtype", ctypes.c_int32)]
-
-
-class _NormParams(ctypes.Structure):
-    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("gain", ctypes.c_void_p),
-                ("shift", ctypes.c_void_p), ("gain_stride", ctypes.c_int64), ("shift_stride", ctypes.c_int64),
-                ("weight_dtype", ctypes.c_int32), ("mod_dtype", ctypes.c_int32), ("gain_offset", ctypes.c_float)]
-
+# veda_rows and veda_norm_params as packed bytes (a third of a ctypes.Structure's cost per call)
+_ROWS = struct.Struct("@Pqqi4x")            # data, batch_stride, row_stride, dtype
+_NORM_PARAMS = struct.Struct("@PPPPqqiif4x")  # weight, bias, gain, shift, 2 strides, 2 types, gain_offset
+_STRIDES3 = struct.Struct("@qqq")
 
 _lib = None
 
@@ -111,6 +106,8 @@ _SIG = {
     "veda_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _Z, _I, _I, _I, _I, _P]),
     "veda_quantize_int8": (_I, [_P, _L, _I, _P, _P, _L, _I, _P]),
     "veda_int8_matmul": (_I, [_P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _I, _P]),
+    "veda_int8_linear_workspace_bytes": (_Z, [_I, _I]),
+    "veda_int8_linear": (_I, [_P, _L, _I, _P, _P, _P, _P, _L, _I, _P, _Z, _I, _I, _I, _P]),
     "veda_check_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "veda_selftest_wait_timeout": (_I, [ctypes.c_uint32, _P]),
 }
@@ -143,14 +140,22 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
+
+
+def _here(t: torch.Tensor) -> bool:
+    """On the calling thread's current device (where the library launches)."""
+    return t.is_cuda and t.get_device() == torch._C._cuda_getDevice()
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, cuda: bool = True,
           shape: Optional[Sequence[int]] = None) -> None:
     """Type, shape, layout and device of a tensor handed to the library: a wrong shape would
     send a kernel outside the buffer, so every one is checked before its pointer is passed."""
+    if t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape) and (not cuda or _here(t)):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(int(x) for x in shape):
@@ -628,6 +633,9 @@ def _need_strided(t: torch.Tensor, name: str, ndim: int, dtype: Optional[torch.d
                   shape: Optional[Sequence[int]] = None, written: bool = False) -> None:
     """Checks of a tensor whose leading dimensions may have any stride: type, shape, device,
     contiguous channels, and, where the library writes it, no two elements in one place."""
+    if ((t.dtype is dtype or dtype is None and t.dtype in _DTYPE) and t.dim() == ndim and (shape is None or t.shape == shape)
+            and (t.is_contiguous() or not written and t.stride(-1) == 1) and _here(t)):
+        return
     if dtype is None and t.dtype not in _DTYPE:
         raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
     if dtype is not None and t.dtype != dtype:
@@ -658,10 +666,15 @@ def _separate(out: torch.Tensor, t: Optional[torch.Tensor], name: str, same_ok: 
         if same_ok:
             return
         raise ValueError(f"out must not be {name}")
-    span = lambda x: (x.data_ptr(), x.data_ptr() + x.element_size() * (1 + sum((n - 1) * s for n, s in zip(x.shape, x.stride()))))
-    a, b = span(out), span(t)
+    a, b = _span(out), _span(t)
     if a[0] < b[1] and b[0] < a[1]:
         raise ValueError(f"out overlaps {name} in memory")
+
+
+def _span(t: torch.Tensor) -> Tuple[int, int]:
+    """First byte and one past the last byte of a tensor's elements."""
+    n = t.numel() if t.is_contiguous() else 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + t.element_size() * n
 
 
 def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -794,17 +807,16 @@ def rotary(x: torch.Tensor, table: RotaryTable, rows: Optional[torch.Tensor] = N
     table._check()
     if out is None:
         out = _new((B, N, H, D), x.dtype, x.device, stream)
-    _need_strided(out, "out", 4, x.dtype, x.shape, written=True)
-    _separate(out, x, "x", True)
-    _separate(out, table.cos_sin, "the table", False)
+    else:
+        _need_strided(out, "out", 4, x.dtype, x.shape, written=True)
+        _separate(out, x, "x", True)
+        _separate(out, table.cos_sin, "the table", False)
     if rows is not None:
         _need(rows, torch.int32, "rows", shape=(B, N))
-    xs = (ctypes.c_int64 * 3)(*x.stride()[:3])
-    ys = (ctypes.c_int64 * 3)(*out.stride()[:3])
     _check("veda_rotary", lib().veda_rotary(
-        _ptr(x), ctypes.addressof(xs), _ptr(out), ctypes.addressof(ys), _DTYPE[x.dtype], _ptr(table.cos_sin),
-        table.rows, _ptr(rows), table.rot_dim, int(table.interleaved), int(bool(inverse)), B, N, H, D,
-        _stream(stream)))
+        _ptr(x), _STRIDES3.pack(*x.stride()[:3]), _ptr(out), _STRIDES3.pack(*out.stride()[:3]), _DTYPE[x.dtype],
+        _ptr(table.cos_sin), table.cos_sin.shape[0], _ptr(rows), 2 * table.cos_sin.shape[1], int(table.interleaved),
+        int(bool(inverse)), B, N, H, D, _stream(stream)))
     return out
 
 
@@ -881,27 +893,33 @@ def _rows3(t: torch.Tensor, name: str, dtype=None, shape=None, written=False) ->
 def _rows(t: Optional[torch.Tensor]):
     if t is None:
         return None
-    return ctypes.byref(_Rows(_ptr(t), t.stride(0), t.stride(1), _DTYPE[t.dtype]))
+    return _ROWS.pack(t.data_ptr(), t.stride(0), t.stride(1), _DTYPE[t.dtype])
 
 
 def _vectors(B: int, C: int, weight, bias, gain, shift, gain_name: str, offset: float):
     """Checked parameters of a norm: weight / bias [C] of one type, gain / shift [B, C] ([C] for
     one sequence) of one type with any batch stride."""
-    for t, n in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _need_strided(t, n, 1, None, (C,))
-    fix = lambda t: t.unsqueeze(0) if t is not None and t.dim() == 1 else t
-    gain, shift = fix(gain), fix(shift)
-    for t, n in ((gain, gain_name), (shift, "shift")):
-        if t is not None:
-            _need_strided(t, n, 2, None, (B, C))
-    for a, b, n in ((weight, bias, "weight and bias"), (gain, shift, f"{gain_name} and shift")):
-        if a is not None and b is not None and a.dtype != b.dtype:
-            raise TypeError(f"{n}: expected one type, got {a.dtype} and {b.dtype}")
-    kind = lambda a, b: _DTYPE[a.dtype] if a is not None else _DTYPE[b.dtype] if b is not None else 2
-    return _NormParams(_ptr(weight), _ptr(bias), _ptr(gain), _ptr(shift),
-                       gain.stride(0) if gain is not None else 0, shift.stride(0) if shift is not None else 0,
-                       kind(weight, bias), kind(gain, shift), offset)
+    wd = md = 2
+    if weight is not None or bias is not None:
+        for t, n in ((weight, "weight"), (bias, "bias")):
+            if t is not None:
+                _need_strided(t, n, 1, None, (C,))
+                wd = _DTYPE[t.dtype]
+        if weight is not None and bias is not None and weight.dtype != bias.dtype:
+            raise TypeError(f"weight and bias: expected one type, got {weight.dtype} and {bias.dtype}")
+    if gain is not None:
+        gain = gain.unsqueeze(0) if gain.dim() == 1 else gain
+        _need_strided(gain, gain_name, 2, None, (B, C))
+        md = _DTYPE[gain.dtype]
+    if shift is not None:
+        shift = shift.unsqueeze(0) if shift.dim() == 1 else shift
+        _need_strided(shift, "shift", 2, None, (B, C))
+        md = _DTYPE[shift.dtype]
+        if gain is not None and gain.dtype != shift.dtype:
+            raise TypeError(f"{gain_name} and shift: expected one type, got {gain.dtype} and {shift.dtype}")
+    return _NORM_PARAMS.pack(_ptr(weight) or 0, _ptr(bias) or 0, _ptr(gain) or 0, _ptr(shift) or 0,
+                             gain.stride(0) if gain is not None else 0, shift.stride(0) if shift is not None else 0,
+                             wd, md, offset)
 
 
 def _norm_kind(kind: str) -> int:
@@ -910,24 +928,24 @@ def _norm_kind(kind: str) -> int:
     return _KIND[kind]
 
 
-def _norm_fwd(x, residual, params, residual_scale, kind, eps, out_dtype, out, want_stats, stream):
-    flat = x.dim() == 2
-    x3 = _rows3(x, "x")
+def _norm_fwd(x, x3, residual, params, residual_scale, kind, eps, out_dtype, out, want_stats, stream):
     B, N, C = x3.shape
     if residual is not None:
         residual = _rows3(residual, "residual", out_dtype, x3.shape)
     if out is None:
-        out = _new(tuple(x.shape), out_dtype, x.device, stream)
-    out3 = _rows3(out, "out", out_dtype, x3.shape, written=True)
-    _separate(out3, x3, "x", True)
-    _separate(out3, residual, "the residual", True)
-    stats = None
+        out = _new(x.shape, out_dtype, x.device, stream)
+        out3 = out if out.dim() == 3 else out.unsqueeze(0)
+    else:
+        out3 = _rows3(out, "out", out_dtype, x3.shape, written=True)
+        _separate(out3, x3, "x", True)
+        _separate(out3, residual, "the residual", True)
+    stats = mean = rstd = None
     if want_stats:
         stats = NormStats(_new((B, N), torch.float32, x.device, stream), _new((B, N), torch.float32, x.device, stream))
+        mean, rstd = stats.mean.data_ptr(), stats.rstd.data_ptr()
     _check("veda_norm_fwd", lib().veda_norm_fwd(
-        _rows(x3), _rows(residual), _rows(out3), ctypes.byref(params), float(residual_scale),
-        _ptr(stats.mean) if stats else None, _ptr(stats.rstd) if stats else None, B, N, C, _norm_kind(kind),
-        float(eps), _stream(stream)))
+        _rows(x3), _rows(residual), _rows(out3), params, residual_scale, mean, rstd, B, N, C, _norm_kind(kind), eps,
+        _stream(stream)))
     return (out, stats) if want_stats else out
 
 
@@ -941,11 +959,10 @@ def norm_modulate(x: torch.Tensor, scale: Optional[torch.Tensor] = None, shift: 
     per sequence (any batch stride: slices of one modulation vector will do); every one of them
     optional. kind "layer", "rms" or "none". ``want_stats`` also returns the ``NormStats`` of
     ``norm_modulate_bwd``. out_dtype: x's type, or bf16 for fp32 x, or fp32 for bf16 x."""
-    x3 = x.unsqueeze(0) if x.dim() == 2 else x
-    _need_strided(x3, "x", 3)
+    x3 = _rows3(x, "x")
     p = _vectors(x3.shape[0], x3.shape[2], weight, bias, scale, shift, "scale", 1.0)
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else x.dtype
-    return _norm_fwd(x, None, p, 0.0, kind, eps, dt, out, want_stats, stream)
+    return _norm_fwd(x, x3, None, p, 0.0, kind, eps, dt, out, want_stats, stream)
 
 
 def norm_gate_add(o: torch.Tensor, residual: torch.Tensor, gate: Optional[torch.Tensor] = None,
@@ -958,38 +975,46 @@ def norm_gate_add(o: torch.Tensor, residual: torch.Tensor, gate: Optional[torch.
     o: the block's output [B, N, C] or [N, C]; residual of the same shape, whose type the result
     has (o's type, or fp32 with bf16 o, or bf16 with fp32 o); gate [B, C]. kind "none" gates o
     itself. ``out`` may be the residual (in place)."""
-    o3 = o.unsqueeze(0) if o.dim() == 2 else o
-    _need_strided(o3, "o", 3)
+    o3 = _rows3(o, "o")
     p = _vectors(o3.shape[0], o3.shape[2], weight, bias, gate, None, "gate", 0.0)
-    return _norm_fwd(o, residual, p, residual_scale, kind, eps, residual.dtype, out, want_stats, stream)
+    return _norm_fwd(o, o3, residual, p, residual_scale, kind, eps, residual.dtype, out, want_stats, stream)
 
 
-def _norm_bwd(dy, x, stats, params, has, residual_grad, residual_scale, kind, out, stream):
-    x3 = _rows3(x, "x")
+def _norm_bwd(dy, x, x3, stats, params, has, residual_grad, residual_scale, kind, out, stream):
     B, N, C = x3.shape
     dy3 = _rows3(dy, "dy", None, x3.shape)
     res3 = None if residual_grad is None else _rows3(residual_grad, "residual_grad", x.dtype, x3.shape)
     k = _norm_kind(kind)
-    if stats is None and k != 2:
-        raise ValueError("stats: the forward's statistics are needed (want_stats=True)")
+    mean = rstd = None
     if stats is not None:
         _need(stats.rstd, torch.float32, "stats.rstd", shape=(B, N))
         _need(stats.mean, torch.float32, "stats.mean", shape=(B, N))
+        mean, rstd = stats.mean.data_ptr(), stats.rstd.data_ptr()
+    elif k != 2:
+        raise ValueError("stats: the forward's statistics are needed (want_stats=True)")
     if out is None:
-        out = _new(tuple(x.shape), x.dtype, x.device, stream)
-    out3 = _rows3(out, "out", x.dtype, x3.shape, written=True)
-    for t, n in ((x3, "x"), (dy3, "dy"), (res3, "residual_grad")):
-        _separate(out3, t, n, True)
-    f32 = lambda want, *shape: _new(shape, torch.float32, x.device, stream) if want else None
-    dgain, dshift = f32(has["gain"], B, C), f32(has["shift"], B, C)
-    dweight, dbias = f32(has["weight"], C), f32(has["bias"], C)
-    nbytes = int(lib().veda_norm_bwd_workspace_bytes(B, N, C))
+        out = _new(x.shape, x.dtype, x.device, stream)
+        out3 = out if out.dim() == 3 else out.unsqueeze(0)
+    else:
+        out3 = _rows3(out, "out", x.dtype, x3.shape, written=True)
+        for t, n in ((x3, "x"), (dy3, "dy"), (res3, "residual_grad")):
+            _separate(out3, t, n, True)
+    gain, shift, weight, bias = has
+    # the gradients of the vectors are rows of one buffer: [B] gain, [B] shift, weight, bias
+    rows = B * gain + B * shift + weight + bias
+    vec = _new((rows, C), torch.float32, x.device, stream)
+    take, at = [], 0
+    for want, n in ((gain, B), (shift, B), (weight, 1), (bias, 1)):
+        take.append(vec[at:at + n] if want else None)
+        at += n * want
+    dgain, dshift, dweight, dbias = take
+    nbytes = lib().veda_norm_bwd_workspace_bytes(B, N, C)
     work = _new((max(nbytes, 16),), torch.uint8, x.device, stream)
     _check("veda_norm_bwd", lib().veda_norm_bwd(
-        _rows(dy3), _rows(x3), _ptr(stats.mean) if stats else None, _ptr(stats.rstd) if stats else None,
-        _rows(res3), _rows(out3), ctypes.byref(params), float(residual_scale), _ptr(dgain), _ptr(dshift),
-        _ptr(dweight), _ptr(dbias), _ptr(work), work.numel(), B, N, C, k, _stream(stream)))
-    return out, dgain, dshift, dweight, dbias
+        _rows(dy3), _rows(x3), mean, rstd, _rows(res3), _rows(out3), params, residual_scale, _ptr(dgain),
+        _ptr(dshift), _ptr(dweight), _ptr(dbias), work.data_ptr(), work.numel(), B, N, C, k, _stream(stream)))
+    one = lambda t: None if t is None else t[0]
+    return out, dgain, dshift, one(dweight), one(dbias)
 
 
 def norm_modulate_bwd(dy: torch.Tensor, x: torch.Tensor, stats: Optional[NormStats],
@@ -1001,11 +1026,10 @@ def norm_modulate_bwd(dy: torch.Tensor, x: torch.Tensor, stats: Optional[NormSta
 
     residual_grad (x's type) is the gradient of the stream that passes the block by: dx gets
     residual_scale times it added, which saves the separate sum."""
-    x3 = x.unsqueeze(0) if x.dim() == 2 else x
-    _need_strided(x3, "x", 3)
+    x3 = _rows3(x, "x")
     p = _vectors(x3.shape[0], x3.shape[2], weight, bias, scale, None, "scale", 1.0)
-    has = dict(gain=scale is not None, shift=want_dshift, weight=weight is not None, bias=bias is not None)
-    dx, dg, dt, dw, db = _norm_bwd(dy, x, stats, p, has, residual_grad, residual_scale, kind, out, stream)
+    has = (scale is not None, bool(want_dshift), weight is not None, bias is not None)
+    dx, dg, dt, dw, db = _norm_bwd(dy, x, x3, stats, p, has, residual_grad, residual_scale, kind, out, stream)
     return NormGrads(dx, dw, db, dscale=dg, dshift=dt)
 
 
@@ -1016,11 +1040,10 @@ def norm_gate_add_bwd(dh: torch.Tensor, o: torch.Tensor, stats: Optional[NormSta
     """Backward of ``norm_gate_add``: dx is the gradient of the block's output o, and dgate,
     dweight, dbias. The residual's gradient is residual_scale dh, which ``norm_modulate_bwd`` of
     the same block adds on its way (residual_grad=dh)."""
-    o3 = o.unsqueeze(0) if o.dim() == 2 else o
-    _need_strided(o3, "o", 3)
+    o3 = _rows3(o, "o")
     p = _vectors(o3.shape[0], o3.shape[2], weight, bias, gate, None, "gate", 0.0)
-    has = dict(gain=gate is not None, shift=False, weight=weight is not None, bias=bias is not None)
-    dx, dg, _, dw, db = _norm_bwd(dh, o, stats, p, has, None, 0.0, kind, out, stream)
+    has = (gate is not None, False, weight is not None, bias is not None)
+    dx, dg, _, dw, db = _norm_bwd(dh, o, o3, stats, p, has, None, 0.0, kind, out, stream)
     return NormGrads(dx, dw, db, dgate=dg)
 
 
@@ -1059,6 +1082,8 @@ class Int8Rows:
 
 def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
     """x [..., K] as a matrix of rows without a copy."""
+    if x.dim() == 2:
+        return x
     if x.dim() < 1:
         raise ValueError(f"{name}: expected at least one dimension")
     try:
@@ -1073,12 +1098,14 @@ def quantize_int8(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) 
     m = _matrix(x, "x")
     _need_strided(m, "x", 2)
     rows, K = m.shape
-    kp = -(-K // 16) * 16
     if out is None:
-        out = Int8Rows(_new((rows, kp), torch.int8, x.device, stream), _new((rows,), torch.float32, x.device, stream), K)
-    if out.K != K or out.rows != rows:
-        raise ValueError(f"out: expected {rows} rows of {K} codes")
-    out._check("out")
+        out = Int8Rows(_new((rows, -(-K // 16) * 16), torch.int8, x.device, stream),
+                       _new((rows,), torch.float32, x.device, stream), K)
+    else:
+        if out.K != K or out.rows != rows:
+            raise ValueError(f"out: expected {rows} rows of {K} codes")
+        out._check("out")
+        _separate(out.codes, m, "x", False)
     _check("veda_quantize_int8", lib().veda_quantize_int8(
         _ptr(m), m.stride(0), _DTYPE[m.dtype], _ptr(out.codes), _ptr(out.scale), rows, K, _stream(stream)))
     return out
@@ -1097,10 +1124,14 @@ def int8_matmul(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
     if bias is not None:
         _need(bias, torch.float32, "bias", shape=(N,))
     if out is None:
+        if out_dtype not in _DTYPE:
+            raise TypeError(f"out_dtype: expected bfloat16, float16 or float32, got {out_dtype}")
         out = _new((M, N), out_dtype, a.codes.device, stream)
-    _need_strided(out, "out", 2, None, (M, N), written=True)
-    for t, n in ((a.codes, "a.codes"), (w.codes, "w.codes"), (a.scale, "a.scale"), (w.scale, "w.scale"), (bias, "bias")):
-        _separate(out, t, n, False)
+    else:
+        _need_strided(out, "out", 2, None, (M, N), written=True)
+        for t, n in ((a.codes, "a.codes"), (w.codes, "w.codes"), (a.scale, "a.scale"), (w.scale, "w.scale"),
+                     (bias, "bias")):
+            _separate(out, t, n, False)
     _check("veda_int8_matmul", lib().veda_int8_matmul(
         _ptr(a.codes), _ptr(a.scale), _ptr(w.codes), _ptr(w.scale), _ptr(bias), _ptr(out),
         out.stride(0), _DTYPE[out.dtype], M, N, a.K, _stream(stream)))
@@ -1109,11 +1140,26 @@ def int8_matmul(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
 
 def int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] = None,
                 out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
-    """x [..., K] W^T + bias in 8-bit integers: ``quantize_int8`` of x's rows, ``int8_matmul`` with
-    the weight's rows; [..., N] in x's type (or out_dtype)."""
-    a = quantize_int8(x, stream=stream)
-    y = int8_matmul(a, w, bias, out_dtype or x.dtype, stream=stream)
-    return y.view(*x.shape[:-1], w.rows)
+    """veda_int8_linear: x [..., K] W^T + bias in 8-bit integers -- ``quantize_int8`` of x's rows and
+    ``int8_matmul`` with the weight's rows in one call; [..., N] in x's type (or out_dtype)."""
+    m = _matrix(x, "x")
+    _need_strided(m, "x", 2)
+    w._check("w")
+    M, K = m.shape
+    N = w.codes.shape[0]
+    if K != w.K:
+        raise ValueError(f"x has rows of {K} values, w of {w.K}")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", shape=(N,))
+    dt = x.dtype if out_dtype is None else out_dtype
+    if dt not in _DTYPE:
+        raise TypeError(f"out_dtype: expected bfloat16, float16 or float32, got {dt}")
+    out = _new((*x.shape[:-1], N), dt, x.device, stream)
+    work = _new((max(16, lib().veda_int8_linear_workspace_bytes(M, K)),), torch.uint8, x.device, stream)
+    _check("veda_int8_linear", lib().veda_int8_linear(
+        m.data_ptr(), m.stride(0), _DTYPE[m.dtype], w.codes.data_ptr(), w.scale.data_ptr(), _ptr(bias),
+        out.data_ptr(), N, _DTYPE[dt], work.data_ptr(), work.numel(), M, N, K, _stream(stream)))
+    return out
 
 
 def check_device_status(stream=None) -> int:

@@ -35,7 +35,7 @@
  *   veda_rotary_unpermute          step 6 with a rotation on the way (the gradients' way back)
  *   veda_norm_fwd, veda_norm_bwd   the norms before and after a block with its scale, shift,
  *                                  gate and residual sum
- *   veda_quantize_int8, veda_int8_matmul  projections in 8-bit integers
+ *   veda_quantize_int8, veda_int8_matmul, veda_int8_linear  projections in 8-bit integers
  *
  * Conventions shared by every call:
  *  - Ownership: the caller allocates and owns every buffer. Pointers named *_dev or
@@ -662,6 +662,21 @@ VEDA_API veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t
  */
 VEDA_API veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w, const float* w_scale,
                                       const float* bias, void* y, int64_t y_stride, int32_t dtype, int32_t M,
+                                      int32_t N, int32_t K, veda_stream_t stream);
+
+/* Workspace bytes of veda_int8_linear: the codes and scales of M rows. */
+VEDA_API size_t veda_int8_linear_workspace_bytes(int32_t M, int32_t K);
+
+/*
+ * veda_quantize_int8 of x's rows and veda_int8_matmul with w's in one call (device); the same
+ * results.
+ *   x          [M][K] of x_dtype, rows x_stride elements apart
+ *   y          [M][N] of y_dtype (device, out), rows y_stride elements apart
+ *   workspace  device scratch of >= veda_int8_linear_workspace_bytes(...) bytes, 16-byte aligned
+ */
+VEDA_API veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, const void* w,
+                                      const float* w_scale, const float* bias, void* y, int64_t y_stride,
+                                      int32_t y_dtype, void* workspace, size_t workspace_bytes, int32_t M,
                                       int32_t N, int32_t K, veda_stream_t stream);
 
 /*

@@ -67,14 +67,11 @@ def test_rotary_tile_refusals(L):
 
 
 def _rows(data=256, b=640, r=64, dtype=0):
-    return ctypes.byref(veda._Rows(data, b, r, dtype))
+    return veda._ROWS.pack(data or 0, b, r, dtype)
 
 
-def _params(**k):
-    d = dict(weight=None, bias=None, gain=None, shift=None, gain_stride=0, shift_stride=0, weight_dtype=2, mod_dtype=2,
-             gain_offset=1.0)
-    d.update(k)
-    return ctypes.byref(veda._NormParams(*[d[f] for f, _ in veda._NormParams._fields_]))
+def _params(weight=0, bias=0, gain=0, shift=0, weight_dtype=2, mod_dtype=2):
+    return veda._NORM_PARAMS.pack(weight, bias, gain, shift, 0, 0, weight_dtype, mod_dtype, 1.0)
 
 
 def test_norm_refusals(L):
@@ -127,6 +124,17 @@ def test_int8_refusals(L):
         assert mm(**bad) == INVALID, bad
     assert mm(K=131072) == UNSUPPORTED
     assert mm(M=0) == OK and mm(N=0) == OK
+
+    need = L.veda_int8_linear_workspace_bytes(4, 60)
+    assert need >= 4 * 64 + 4 * 4 and L.veda_int8_linear_workspace_bytes(0, 60) == 0
+
+    def lin(x=256, st=64, xdt=0, w=16, sw=16, bias=None, y=16, ys=32, dt=0, ws=16, nws=need, M=4, N=32, K=60):
+        return L.veda_int8_linear(x, st, xdt, w, sw, bias, y, ys, dt, ws, nws, M, N, K, None)
+    for bad in (dict(x=None), dict(w=None), dict(sw=None), dict(y=None), dict(ws=None), dict(ws=8), dict(nws=need - 1),
+                dict(x=255), dict(w=8), dict(xdt=3), dict(dt=-1), dict(M=-1), dict(K=0), dict(ys=31), dict(bias=2)):
+        assert lin(**bad) == INVALID, bad
+    assert lin(K=131072, nws=2**40) == UNSUPPORTED
+    assert lin(M=0, x=None, ws=None, nws=0) == OK and lin(N=0) == OK
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU behaviour")
