@@ -20,8 +20,12 @@ namespace veda {
 namespace int8 {
 
 // ------------------------------------------------------------------------------------
-// Row quantisation. A row belongs to a warp (K <= 1024) or to a CTA of 128 threads; it is held
-// in registers between the maximum and the rounding (rows over 8,192 are read again, from L2).
+// Row quantisation: HBM bound (one read of the row, one write of its codes). A row of up to 8,192
+// values belongs to a group of threads -- a warp up to 1,024 values, a CTA above -- whose thread i
+// owns the 8-value vectors i, i + threads, ...: rows run through a ring of kQuantStages rows in
+// shared memory that each thread fills for itself with asynchronous copies, so the next rows are
+// on their way while one is rounded. Longer rows, and rows that start on no 16-byte boundary, are
+// read twice with plain loads.
 // The division is exact: x * (1 / scale) is rounded, and where that product lies next to a half the
 // sign of the exactly rounded x - scale (q +- 1/2) decides, ties to even.
 // A row with a NaN or an infinity gets scale NaN (and codes 0), so its outputs are NaN; a row
@@ -38,8 +42,10 @@ struct QuantArgs {
 };
 
 constexpr int kQuantWarpK = 1024;
-constexpr int kQuantThreads = 128;
-constexpr int kQuantHeld = 8;      // vectors of 8 held per thread (CTA rows)
+constexpr int kQuantMaxK = 8192;      // ring kernels
+constexpr int kQuantVecs = 4;         // vectors a thread
+constexpr int kQuantThreads = 256;    // most threads of a CTA
+constexpr int kQuantStages = 3;
 
 template <typename T>
 __device__ __forceinline__ void load8(const T* row, int32_t k0, int32_t K, bool vec, float* f) {
@@ -113,81 +119,131 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits, bool& live) {
   return __fdiv_rn(amax, 127.0f);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) quant_warp_kernel(const QuantArgs a) {
-  constexpr int NV = kQuantWarpK / 256;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= a.rows) return;
-  const int32_t lane = threadIdx.x & 31;
-  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  float f[NV][8];
-  uint32_t m = 0;
+// Largest |x| of a vector, as bits (packed for the 16-bit types, whose order is their bits').
+template <typename T> struct AbsMax {
+  uint32_t m = 0u;
+  __device__ __forceinline__ void add(const uint4& v) {
+    const uint32_t mask = 0x7fff7fffu;
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & mask, v.y & mask), __vmaxu2(v.z & mask, v.w & mask)));
+  }
+  __device__ __forceinline__ uint32_t bits() const {
+    const uint16_t b = static_cast<uint16_t>(max(m & 0xffffu, m >> 16));
+    return __float_as_uint(rotary::Vec<T>::one(*reinterpret_cast<const T*>(&b))) & 0x7fffffffu;
+  }
+};
+template <> struct AbsMax<float> {
+  uint32_t m = 0u;
+  __device__ __forceinline__ void add(const uint4& v) {
+    const uint32_t mask = 0x7fffffffu;
+    m = max(m, max(max(v.x & mask, v.y & mask), max(v.z & mask, v.w & mask)));
+  }
+  __device__ __forceinline__ uint32_t bits() const { return m; }
+};
+
+// kWarp: a row per warp, else a row per CTA. Rows start on 16-byte boundaries.
+template <typename T, bool kWarp>
+__global__ void __launch_bounds__(kQuantThreads) quant_ring_kernel(const QuantArgs a) {
+  using V = rotary::Vec<T>;
+  constexpr int U = 8 / V::E;                                  // 16-byte units a vector
+  constexpr int kStage = kQuantVecs * U;                       // units a thread and row
+  extern __shared__ __align__(16) uint8_t quant_smem[];
+  __shared__ uint32_t red[2][kQuantThreads / 32];
+  const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
+  const int32_t me = kWarp ? (threadIdx.x & 31) : threadIdx.x, warps = blockDim.x >> 5;
+  uint4* ring = reinterpret_cast<uint4*>(quant_smem) + (kWarp ? (threadIdx.x >> 5) * kQuantStages * kStage * 32 : 0) + me;
+  const int64_t step = kWarp ? static_cast<int64_t>(gridDim.x) * warps : gridDim.x;
+  const int64_t first = kWarp ? static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5) : blockIdx.x;
+
+  const auto fetch = [&](int64_t row, int st) {
+    if (row < a.rows) {
+      const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+      uint4* slot = ring + st * kStage * threads;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int32_t k0 = (lane + 32 * j) * 8;
-    if (k0 < a.kp) load8<T>(x, k0, a.K, a.vec != 0, f[j]);
-    if (k0 < a.kp) {
+      for (int j = 0; j < kQuantVecs; ++j) {
+        const int32_t k0 = (me + j * threads) * 8;
+        if (k0 + 8 <= a.K) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[j][i]));
+          for (int u = 0; u < U; ++u)
+            rotary::copy16_async(smem_u32(slot + (j * U + u) * threads), reinterpret_cast<const uint4*>(x + k0) + u);
+        } else if (k0 < a.kp) {                                // the row's end: zeros behind K
+          uint4 tmp[U];
+          T* t = reinterpret_cast<T*>(tmp);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = k0 + i < a.K ? x[k0 + i] : V::to(0.f);
+#pragma unroll
+          for (int u = 0; u < U; ++u) slot[(j * U + u) * threads] = tmp[u];
+        }
+      }
     }
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  bool live;
-  const float s = row_scale(m, live);
-  const float inv = 1.0f / s;
-  int8_t* out = a.codes + row * a.kp;
+    rotary::copies_commit();
+  };
+  for (int i = 0; i < kQuantStages - 1; ++i) fetch(first + i * step, i);
+  int st = 0, flip = 0;
+  for (int64_t row = first; row < a.rows; row += step) {
+    rotary::copies_wait<kQuantStages - 2>();
+    const uint4* slot = ring + st * kStage * threads;
+    uint4 raw[kQuantVecs][U];
+    AbsMax<T> big;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int32_t k0 = (lane + 32 * j) * 8;
-    if (k0 < a.kp) *reinterpret_cast<uint2*>(out + k0) = codes8(f[j], s, inv, live);
+    for (int j = 0; j < kQuantVecs; ++j) {
+      const bool own = (me + j * threads) * 8 < a.kp;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        raw[j][u] = own ? slot[(j * U + u) * threads] : make_uint4(0, 0, 0, 0);
+        big.add(raw[j][u]);
+      }
+    }
+    fetch(row + (kQuantStages - 1) * step, st == 0 ? kQuantStages - 1 : st - 1);   // read last round
+    uint32_t m = __reduce_max_sync(0xffffffffu, big.bits());
+    if (!kWarp) {
+      if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = m;
+      __syncthreads();
+      for (int32_t w = 0; w < warps; ++w) m = max(m, red[flip][w]);
+      flip ^= 1;
+    }
+    bool live;
+    const float s = row_scale(m, live);
+    const float inv = 1.0f / s;
+    int8_t* out = a.codes + row * a.kp;
+#pragma unroll
+    for (int j = 0; j < kQuantVecs; ++j) {
+      const int32_t k0 = (me + j * threads) * 8;
+      if (k0 >= a.kp) continue;
+      float f[8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) V::get(raw[j][u], f + u * V::E);
+      *reinterpret_cast<uint2*>(out + k0) = codes8(f, s, inv, live);
+    }
+    if (me == 0) a.scale[row] = s;
+    st = st == kQuantStages - 1 ? 0 : st + 1;
   }
-  if (lane == 0) a.scale[row] = s;
+  rotary::copies_wait<0>();
 }
 
+// Any row: a CTA reads it twice.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) quant_row_kernel(const QuantArgs a) {
   __shared__ uint32_t red[kQuantThreads / 32];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-  float f[kQuantHeld][8];
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < kQuantHeld; ++j) {
-    const int32_t k0 = (static_cast<int32_t>(threadIdx.x) + kQuantThreads * j) * 8;
-    if (k0 < a.kp) {
-      load8<T>(x, k0, a.K, a.vec != 0, f[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[j][i]));
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    uint32_t m = 0;
+    for (int32_t k = threadIdx.x; k < a.K; k += blockDim.x) m = max(m, abs_bits(rotary::Vec<T>::one(x[k])));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int32_t w = 0; w < static_cast<int32_t>(blockDim.x >> 5); ++w) m = max(m, red[w]);
+    bool live;
+    const float s = row_scale(m, live);
+    const float inv = 1.0f / s;
+    int8_t* out = a.codes + row * a.kp;
+    for (int32_t k0 = threadIdx.x * 8; k0 < a.kp; k0 += blockDim.x * 8) {
+      float f[8];
+      load8<T>(x, k0, a.K, a.vec != 0, f);
+      *reinterpret_cast<uint2*>(out + k0) = codes8(f, s, inv, live);
     }
+    if (threadIdx.x == 0) a.scale[row] = s;
+    __syncthreads();                                           // red is read before the next row's maxima
   }
-  for (int32_t k0 = (static_cast<int32_t>(threadIdx.x) + kQuantThreads * kQuantHeld) * 8; k0 < a.kp;
-       k0 += kQuantThreads * 8) {
-    float g[8];
-    load8<T>(x, k0, a.K, a.vec != 0, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(g[i]));
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, red[w]);
-  bool live;
-  const float s = row_scale(m, live);
-  const float inv = 1.0f / s;
-  int8_t* out = a.codes + row * a.kp;
-#pragma unroll
-  for (int j = 0; j < kQuantHeld; ++j) {
-    const int32_t k0 = (static_cast<int32_t>(threadIdx.x) + kQuantThreads * j) * 8;
-    if (k0 < a.kp) *reinterpret_cast<uint2*>(out + k0) = codes8(f[j], s, inv, live);
-  }
-  for (int32_t k0 = (static_cast<int32_t>(threadIdx.x) + kQuantThreads * kQuantHeld) * 8; k0 < a.kp;
-       k0 += kQuantThreads * 8) {
-    float g[8];
-    load8<T>(x, k0, a.K, a.vec != 0, g);
-    *reinterpret_cast<uint2*>(out + k0) = codes8(g, s, inv, live);
-  }
-  if (threadIdx.x == 0) a.scale[row] = s;
 }
 
 // ------------------------------------------------------------------------------------

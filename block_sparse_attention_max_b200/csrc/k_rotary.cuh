@@ -11,10 +11,9 @@
 //
 // Everything here streams HBM: a pair costs four multiply-adds for the 4 to 8 bytes it reads
 // and writes. What matters is that every access is a 16-byte vector, that enough of them are in
-// flight, and that the table (rot_dim * 4 bytes a token, read by every head) is taken from the
-// caches: the plain kernel loads a token's cos / sin into registers once and loops over heads;
-// in the tile kernels the CTAs that run together hold the same tile of different heads, so the
-// table's rows come from L2.
+// flight, and that the table (rot_dim * 4 bytes a token, read by every head) is fetched once for
+// several heads: the raster kernel loads a token's cos / sin into registers and loops over heads;
+// the tile kernels copy the rows of a tile's tokens into shared memory for eight heads.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -269,198 +268,345 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------------------------
-// Rotation of one 16-byte chunk (channels 8c .. 8c+7) of a bf16 row whose 16 chunks lie in the
-// 16 lanes of a half warp. Interleaved pairs are inside the chunk; in the half layout the
-// partner chunk is P / 8 lanes away and comes by shuffle (all 32 lanes take part). `cs` is the
-// token's table row; `live` is false for a slot without a token, whose chunk is zero.
+// The tile kernels. A CTA takes one tile of up to 8 neighbouring heads, a warp a head; the tile's
+// 128 rows go by in batches of 8, and the batches of a CTA's tiles form one stream: while one is
+// turned and written, the next one's rows (each warp's own) and its rows of the table (one copy
+// for the CTA) are on their way into the other buffer by asynchronous copies, and the token indices
+// of the batch after that are on their way into a register.
+//
+// The table is what decides the speed: a token's row of it has rot_dim * 4 bytes, twice the 256
+// bytes of the row it turns. Read by every head from L2, 8 to 16 rows in registers at a time, the
+// gather of the 16:9 clip took 378 us a tensor. Neighbouring heads mostly have the same tile map,
+// so the CTA copies the rows of its first head's tokens once; a warp whose head has another token
+// in that slot (per-head tile orders) reads that row of the table from global memory instead.
+//
+// A half warp turns one token row; a lane holds two pieces of four channels, chosen so that both
+// halves of a pair are its own and that a warp's accesses of row and table are contiguous:
+// interleaved pairs, channels 4c and 64 + 4c; half layout, channels 4c and P + 4c (the rest of the
+// lanes carry the channels behind the turned ones).
 // ------------------------------------------------------------------------------------
-template <bool kHalf>
-struct Turn {
-  static constexpr int kPairs = kHalf ? 8 : 4;   // pairs whose cos / sin the chunk needs
-  int32_t p0;        // first pair of this chunk
-  int32_t partner;   // lane holding the partner chunk (half layout)
-  float s_sign;      // sign of the partner's term
-  bool turned;       // chunk inside the rotated part
-
-  __device__ __forceinline__ Turn(int32_t c, uint32_t lane, int32_t P, float sign) {
-    if (kHalf) {
-      const int32_t hc = P / 8;
-      turned = c < 2 * hc;
-      const bool first = c < hc;
-      p0 = (first ? c : c - hc) * 8;
-      partner = static_cast<int32_t>(lane) + (first ? hc : -hc);
-      if (!turned) { p0 = 0; partner = static_cast<int32_t>(lane); }
-      s_sign = first ? -sign : sign;
-    } else {
-      turned = c < P / 4;
-      p0 = turned ? 4 * c : 0;
-      partner = static_cast<int32_t>(lane);
-      s_sign = sign;
-    }
-  }
-
-  struct CosSin { float4 v[kPairs / 2]; };
-  __device__ __forceinline__ void load(CosSin& t, const float2* row, bool live) const {
-    const float4* p = reinterpret_cast<const float4*>(row + p0);
-#pragma unroll
-    for (int i = 0; i < kPairs / 2; ++i)
-      t.v[i] = live && turned ? __ldg(p + i) : make_float4(1.f, 0.f, 1.f, 0.f);
-  }
-
-  __device__ __forceinline__ void apply(const uint4& raw, const CosSin& t, float* f) const {
-    Vec<__nv_bfloat16>::get(raw, f);
-    if (kHalf) {
-      uint4 o;
-      o.x = __shfl_sync(0xffffffffu, raw.x, partner);
-      o.y = __shfl_sync(0xffffffffu, raw.y, partner);
-      o.z = __shfl_sync(0xffffffffu, raw.z, partner);
-      o.w = __shfl_sync(0xffffffffu, raw.w, partner);
-      float g[8];
-      Vec<__nv_bfloat16>::get(o, g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 cs = t.v[kHalf ? i : 0];
-        f[2 * i] = fmaf(f[2 * i], cs.x, g[2 * i] * (cs.y * s_sign));
-        f[2 * i + 1] = fmaf(f[2 * i + 1], cs.z, g[2 * i + 1] * (cs.w * s_sign));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 cs = t.v[i];
-        const float a0 = f[4 * i], a1 = f[4 * i + 1], b0 = f[4 * i + 2], b1 = f[4 * i + 3];
-        f[4 * i] = fmaf(a0, cs.x, -(a1 * (cs.y * s_sign)));
-        f[4 * i + 1] = fmaf(a1, cs.x, a0 * (cs.y * s_sign));
-        f[4 * i + 2] = fmaf(b0, cs.z, -(b1 * (cs.w * s_sign)));
-        f[4 * i + 3] = fmaf(b1, cs.z, b0 * (cs.w * s_sign));
-      }
-    }
-  }
-};
-
 struct TileArgs {
-  GatherArgs g;
+  GatherArgs g;            // units: B * nT * groups
   const int32_t* valid;    // [H][nT] (gather only)
   float* pooled;           // [B][H][nT][3][128] (gather only)
   const float2* cs;        // [table_rows][P]
   int64_t batch_rows;      // 0 (table shared by the batch) or N
   int32_t P;
+  int32_t groups, hg;      // head groups, heads per group (warps per CTA)
   float sign;
 };
 
-// Steps 1 + 2 with the rotation on the way: permute_pool_kernel's work split (one warp per
-// tile, 16 rows a pass, partials in registers). The pooled mean / max / min are taken from the
-// fp32 values before they are rounded for the tile.
-template <bool kHalf>
-__global__ void __launch_bounds__(kPoolThreads) rotary_permute_pool_kernel(const __grid_constant__ TileArgs p) {
+constexpr int kTileHeads = 8;
+constexpr int kBatchRows = 8;
+// one buffer: hg warps' rows, then the table's rows
+__host__ __device__ constexpr uint32_t tile_buffer_bytes(int32_t hg, int32_t P) {
+  return static_cast<uint32_t>(hg) * kBatchRows * kRowBytes + kBatchRows * static_cast<uint32_t>(P) * 8u;
+}
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_v2(void* p, uint2 v) {
+  asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void unpack4(uint2 v, float* f) {
+  f[0] = __uint_as_float(v.x << 16);
+  f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16);
+  f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+// Place in a CTA's stream of batches.
+struct TileBatch {
+  int64_t u;
+  int32_t r0, b, h0, t;
+  __device__ __forceinline__ void at(int64_t unit, const TileArgs& p) {
+    u = unit;
+    r0 = 0;
+    if (u >= p.g.units) return;
+    const int64_t bt = u / p.groups;
+    h0 = static_cast<int32_t>(u - bt * p.groups) * p.hg;
+    b = static_cast<int32_t>(bt / p.g.nT);
+    t = static_cast<int32_t>(bt - static_cast<int64_t>(b) * p.g.nT);
+  }
+  __device__ __forceinline__ void advance(const TileArgs& p) {
+    r0 += kBatchRows;
+    if (r0 == 128) at(u + gridDim.x, p);
+  }
+  // lanes r and 8 + r: token of slot r0 + r of head h0 + warp; lanes 16 + r and 24 + r: of head h0.
+  // -1 where there is none (past the stream, past the heads, pad slots).
+  __device__ __forceinline__ int32_t token(const TileArgs& p, uint32_t warp, uint32_t lane) const {
+    const int32_t h = h0 + (lane < 16 ? static_cast<int32_t>(warp) : 0);
+    if (u >= p.g.units || h >= p.g.H) return -1;
+    return __ldg(p.g.map + static_cast<int64_t>(h) * p.g.Npad + static_cast<int64_t>(t) * 128 + r0 + (lane & (kBatchRows - 1)));
+  }
+};
+
+// kGather: steps 1 + 2 with the rotation on the way; the pooled mean / max / min are taken from the
+// fp32 values before they are rounded for the tile. Otherwise step 6 with a rotation on the way
+// (sign -1: the transpose, which takes dQ and dK in tile order to raster order and through the
+// rotary positions in one pass).
+// kFull: all 128 channels are turned (P = 64).
+template <bool kHalf, bool kGather, bool kFull>
+__global__ void __launch_bounds__(32 * kTileHeads, 3) rotary_tiles_kernel(const __grid_constant__ TileArgs p) {
+  extern __shared__ __align__(16) uint8_t tile_smem[];
   const GatherArgs& a = p.g;
-  const uint32_t lane = threadIdx.x & 31;
-  const uint32_t c = lane & 15, half = lane >> 4;
-  const Turn<kHalf> turn(static_cast<int32_t>(c), lane, p.P, p.sign);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kPoolThreads / 32);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kPoolThreads / 32) + (threadIdx.x >> 5); u < a.units;
-       u += warps) {
-    int32_t b, h, t;
-    unit_coords(u, a.H, a.nT, b, h, t);
-    const int64_t lin = (static_cast<int64_t>(b) * a.H + h) * a.nT + t;
-    int32_t nv = p.valid[static_cast<int64_t>(h) * a.nT + t];
-    nv = nv < 0 ? 0 : (nv > 128 ? 128 : nv);
-    const int32_t* m = a.map + static_cast<int64_t>(h) * a.Npad + static_cast<int64_t>(t) * 128 + half;
-    const uint8_t* src = a.src + (static_cast<int64_t>(b) * a.N * a.H + h) * kRowBytes + c * 16;
-    const int64_t tok_stride = static_cast<int64_t>(a.H) * kRowBytes;
-    const float2* cs = p.cs + b * p.batch_rows * p.P;
-    uint8_t* dst = a.dst + lin * kTileBytes + half * kRowBytes + c * 16;
-    float sum[8], mx[8], mn[8];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t c = static_cast<int32_t>(lane & 15), half = static_cast<int32_t>(lane >> 4);
+  // this lane's two pieces: first channels, first pairs, whether turned
+  const int32_t P = kFull ? 64 : p.P;
+  int32_t o1, o2, p1, p2;
+  bool t1, t2;
+  if (kHalf) {
+    t1 = t2 = 4 * c < P;
+    o1 = t1 ? 4 * c : 2 * P + 8 * (c - P / 4);
+    o2 = t1 ? P + 4 * c : o1 + 4;
+    p1 = t1 ? 4 * c : 0;
+    p2 = p1 + 2;
+  } else {
+    o1 = 4 * c;
+    o2 = 64 + 4 * c;
+    t1 = o1 < 2 * P;
+    t2 = o2 < 2 * P;
+    p1 = t1 ? 2 * c : 0;
+    p2 = t2 ? 32 + 2 * c : 0;
+  }
+  const uint32_t buffer = tile_buffer_bytes(p.hg, P);
+  const uint32_t table = static_cast<uint32_t>(p.hg) * kBatchRows * kRowBytes;    // offset in a buffer
+  const uint32_t sb = smem_u32(tile_smem), mine = sb + warp * kBatchRows * kRowBytes;
+  const int64_t token_bytes = static_cast<int64_t>(a.H) * kRowBytes;
+  const int32_t row_units = P / 2;                                                // 16-byte units a table row
+
+  const auto checked = [&](int32_t tok) {
+    if (tok >= a.N) {
+      if (lane < 16) flag_status(ST_BAD_MAP);
+      return -1;
+    }
+    return tok;
+  };
+  const auto issue = [&](const TileBatch& q, int32_t tok, uint32_t k) {
+    if (q.u < a.units) {
+      const int32_t h = q.h0 + static_cast<int32_t>(warp);
+      const uint8_t* raster = a.src + (static_cast<int64_t>(q.b) * a.N * a.H + h) * kRowBytes + c * 16;
+      const uint8_t* tile = a.src + ((static_cast<int64_t>(q.b) * a.H + h) * a.Npad + static_cast<int64_t>(q.t) * 128 + q.r0) * kRowBytes + c * 16;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) { sum[k] = 0.f; mx[k] = -INFINITY; mn[k] = INFINITY; }
-#pragma unroll 1
-    for (int32_t r0 = 0; r0 < 128; r0 += 16) {
-      int32_t tok[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) tok[i] = __ldg(m + r0 + 2 * i);
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (tok[i] >= a.N) flag_status(ST_BAD_MAP);
-        if (tok[i] >= a.N) tok[i] = -1;
-        if (tok[i] >= 0) v[i] = ld_stream(src + tok[i] * tok_stride);
+      for (int i = 0; i < kBatchRows / 2; ++i) {
+        const int32_t tk = __shfl_sync(0xffffffffu, tok, 2 * i + half);
+        if (tk >= 0)
+          copy16_async(mine + k * buffer + (2 * i + half) * kRowBytes + c * 16,
+                       kGather ? raster + tk * token_bytes : tile + (2 * i + half) * kRowBytes);
       }
+      const float2* cs = p.cs + q.b * p.batch_rows * P;
+      for (int32_t i = static_cast<int32_t>(threadIdx.x); i < kBatchRows * row_units; i += 32 * p.hg) {   // whole warps
+        const int32_t r = i / row_units, o = i - r * row_units;
+        const int32_t tk = __shfl_sync(0xffffffffu, tok, 16 + r);
+        if (tk >= 0)
+          copy16_async(sb + k * buffer + table + static_cast<uint32_t>(i) * 16, reinterpret_cast<const float4*>(cs + static_cast<int64_t>(tk) * P) + o);
+      }
+    }
+    copies_commit();
+  };
+
+  TileBatch cur, nxt, far;
+  cur.at(blockIdx.x, p);
+  int32_t tok_cur = checked(cur.token(p, warp, lane));
+  issue(cur, tok_cur, 0);
+  nxt = cur;
+  nxt.advance(p);
+  int32_t tok_nxt = checked(nxt.token(p, warp, lane));
+  far = nxt;
+  uint32_t k = 0;
+  float sum[8], mx[8], mn[8];
+  int32_t nv = 0;
+  while (cur.u < a.units) {
+    far.advance(p);
+    const int32_t tok_far = far.token(p, warp, lane);
+    copies_wait<0>();
+    __syncthreads();            // the batch is here for the whole CTA, and the other buffer is free
+    issue(nxt, tok_nxt, k ^ 1);
+    const int32_t h = cur.h0 + static_cast<int32_t>(warp);
+    if (h < a.H) {
+      if (kGather && cur.r0 == 0) {
+        nv = __ldg(p.valid + static_cast<int64_t>(h) * a.nT + cur.t);
+        nv = nv < 0 ? 0 : (nv > 128 ? 128 : nv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        typename Turn<kHalf>::CosSin t4;
-        turn.load(t4, cs + static_cast<int64_t>(tok[i] < 0 ? 0 : tok[i]) * p.P, tok[i] >= 0);
+        for (int i = 0; i < 8; ++i) { sum[i] = 0.f; mx[i] = -INFINITY; mn[i] = INFINITY; }
+      }
+      const int64_t lin = (static_cast<int64_t>(cur.b) * a.H + h) * a.nT + cur.t;
+      uint8_t* tile = a.dst + lin * kTileBytes + (cur.r0 + half) * kRowBytes;
+      uint8_t* raster = a.dst + (static_cast<int64_t>(cur.b) * a.N * a.H + h) * kRowBytes;
+      const float2* cs = p.cs + cur.b * p.batch_rows * P;
+      const uint32_t src1 = mine + k * buffer + half * kRowBytes + o1 * 2, src2 = src1 + (o2 - o1) * 2;
+      const uint32_t row1 = sb + k * buffer + table + static_cast<uint32_t>(half * P + p1) * 8u, row2 = row1 + (p2 - p1) * 8;
+      // row 2 i + half, turned: the pieces as written and, in fp32, g
+      const auto turn_row = [&](int i, const float4& ta, const float4& tb, float* g, uint2& v1, uint2& v2) {
+        v1 = ld_shared8(src1 + i * 2 * kRowBytes);
+        v2 = ld_shared8(src2 + i * 2 * kRowBytes);
         float f[8];
-        turn.apply(v[i], t4, f);
-        st_v4(dst + (r0 + 2 * i) * kRowBytes, turn.turned ? Vec<__nv_bfloat16>::put(f) : v[i]);
-        if (r0 + static_cast<int32_t>(half) + 2 * i < nv) {
+        unpack4(v1, f);
+        unpack4(v2, f + 4);
+        float4 ca = ta, cb = tb;
+        if (!kGather) { ca.y *= p.sign; ca.w *= p.sign; cb.y *= p.sign; cb.w *= p.sign; }   // gather: +1
+        if (kHalf) {            // pairs (f[e], f[4 + e]), cos / sin (ca, ca, cb, cb)
+          g[0] = fmaf(f[0], ca.x, -(f[4] * ca.y)); g[4] = fmaf(f[4], ca.x, f[0] * ca.y);
+          g[1] = fmaf(f[1], ca.z, -(f[5] * ca.w)); g[5] = fmaf(f[5], ca.z, f[1] * ca.w);
+          g[2] = fmaf(f[2], cb.x, -(f[6] * cb.y)); g[6] = fmaf(f[6], cb.x, f[2] * cb.y);
+          g[3] = fmaf(f[3], cb.z, -(f[7] * cb.w)); g[7] = fmaf(f[7], cb.z, f[3] * cb.w);
+        } else {
+          g[0] = fmaf(f[0], ca.x, -(f[1] * ca.y)); g[1] = fmaf(f[1], ca.x, f[0] * ca.y);
+          g[2] = fmaf(f[2], ca.z, -(f[3] * ca.w)); g[3] = fmaf(f[3], ca.z, f[2] * ca.w);
+          g[4] = fmaf(f[4], cb.x, -(f[5] * cb.y)); g[5] = fmaf(f[5], cb.x, f[4] * cb.y);
+          g[6] = fmaf(f[6], cb.z, -(f[7] * cb.w)); g[7] = fmaf(f[7], cb.z, f[6] * cb.w);
+        }
+        if (kFull || t1) {
+          v1 = make_uint2(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]));
+        } else {                // behind the turned channels: the bits as they are
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            sum[k] += f[k];
-            mx[k] = fmaxf(mx[k], f[k]);
-            mn[k] = fminf(mn[k], f[k]);
+          for (int e = 0; e < 4; ++e) g[e] = f[e];
+        }
+        if (kFull || t2) {
+          v2 = make_uint2(pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
+        } else {
+#pragma unroll
+          for (int e = 4; e < 8; ++e) g[e] = f[e];
+        }
+      };
+      uint8_t* tile1 = tile + o1 * 2;
+      uint8_t* tile2 = tile + o2 * 2;
+      // three kinds of batch, by one vote: every slot's token is that of the CTA's first head (whose
+      // table rows are in shared memory), no slot has a token, and the rest, row by row
+      const int32_t first_head = __shfl_sync(0xffffffffu, tok_cur, 16 + c);
+      const bool same = __all_sync(0xffffffffu, tok_cur >= 0 && tok_cur == first_head) &&
+                        (!kGather || nv >= cur.r0 + kBatchRows);
+      if (same) {
+#pragma unroll
+        for (int i = 0; i < kBatchRows / 2; i += 2) {      // two rows at a time: three-input max / min
+          float g[8], q[8];
+          uint2 v1, v2;
+          turn_row(i, ld_shared_f4(row1 + i * 16 * P), ld_shared_f4(row2 + i * 16 * P), g, v1, v2);
+          if (kGather) {
+            st_v2(tile1 + 2 * i * kRowBytes, v1);
+            st_v2(tile2 + 2 * i * kRowBytes, v2);
+          } else {
+            uint8_t* dst = raster + __shfl_sync(0xffffffffu, tok_cur, 2 * i + half) * token_bytes;
+            st_v2(dst + o1 * 2, v1);
+            st_v2(dst + o2 * 2, v2);
+          }
+          turn_row(i + 1, ld_shared_f4(row1 + (i + 1) * 16 * P), ld_shared_f4(row2 + (i + 1) * 16 * P), q, v1, v2);
+          if (kGather) {
+            st_v2(tile1 + (2 * i + 2) * kRowBytes, v1);
+            st_v2(tile2 + (2 * i + 2) * kRowBytes, v2);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              sum[e] += g[e] + q[e];
+              mx[e] = fmax3(mx[e], g[e], q[e]);
+              mn[e] = fmin3(mn[e], g[e], q[e]);
+            }
+          } else {
+            uint8_t* dst = raster + __shfl_sync(0xffffffffu, tok_cur, 2 * i + 2 + half) * token_bytes;
+            st_v2(dst + o1 * 2, v1);
+            st_v2(dst + o2 * 2, v2);
+          }
+        }
+      } else if (__all_sync(0xffffffffu, tok_cur < 0 || lane >= 16) && (!kGather || nv <= cur.r0)) {
+        if (kGather) {
+#pragma unroll
+          for (int i = 0; i < kBatchRows / 2; ++i) {
+            st_v2(tile1 + 2 * i * kRowBytes, make_uint2(0, 0));
+            st_v2(tile2 + 2 * i * kRowBytes, make_uint2(0, 0));
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kBatchRows / 2; ++i) {
+          const int32_t r = 2 * i + half;
+          const int32_t tk = __shfl_sync(0xffffffffu, tok_cur, r), lead = __shfl_sync(0xffffffffu, tok_cur, 16 + r);
+          float g[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] = 0.f;
+          uint2 v1 = make_uint2(0, 0), v2 = v1;
+          if (tk >= 0) {
+            float4 ca, cb;
+            if (tk == lead) {
+              ca = ld_shared_f4(row1 + i * 16 * P);
+              cb = ld_shared_f4(row2 + i * 16 * P);
+            } else {
+              const float2* row = cs + static_cast<int64_t>(tk) * P;
+              ca = __ldg(reinterpret_cast<const float4*>(row + p1));
+              cb = __ldg(reinterpret_cast<const float4*>(row + p2));
+            }
+            turn_row(i, ca, cb, g, v1, v2);
+          }
+          if (kGather) {
+            st_v2(tile1 + 2 * i * kRowBytes, v1);
+            st_v2(tile2 + 2 * i * kRowBytes, v2);
+            if (cur.r0 + r < nv) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                sum[e] += g[e];
+                mx[e] = fmaxf(mx[e], g[e]);
+                mn[e] = fminf(mn[e], g[e]);
+              }
+            }
+          } else if (tk >= 0) {
+            uint8_t* dst = raster + tk * token_bytes;
+            st_v2(dst + o1 * 2, v1);
+            st_v2(dst + o2 * 2, v2);
           }
         }
       }
-    }
+      if (kGather && cur.r0 == 128 - kBatchRows) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 16);
-      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 16));
-      mn[k] = fminf(mn[k], __shfl_xor_sync(0xffffffffu, mn[k], 16));
-    }
-    if (half == 0) {
-      float4* o = reinterpret_cast<float4*>(p.pooled + lin * 384 + c * 8);
-      const float inv = nv > 0 ? 1.0f / static_cast<float>(nv) : 0.f;
-      if (nv == 0) {
+        for (int e = 0; e < 8; ++e) {
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 16);
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+          mn[e] = fminf(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], 16));
+        }
+        if (half == 0) {
+          float* o = p.pooled + lin * 384;
+          const float inv = nv > 0 ? 1.0f / static_cast<float>(nv) : 0.f;
+          if (nv == 0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx[k] = mn[k] = 0.f;
+            for (int e = 0; e < 8; ++e) mx[e] = mn[e] = 0.f;
+          }
+          const auto put = [&](int32_t at, float x, float y, float z, float w) {
+            *reinterpret_cast<float4*>(o + at) = make_float4(x, y, z, w);
+          };
+          put(o1, sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
+          put(o2, sum[4] * inv, sum[5] * inv, sum[6] * inv, sum[7] * inv);
+          put(128 + o1, mx[0], mx[1], mx[2], mx[3]);
+          put(128 + o2, mx[4], mx[5], mx[6], mx[7]);
+          put(256 + o1, mn[0], mn[1], mn[2], mn[3]);
+          put(256 + o2, mn[4], mn[5], mn[6], mn[7]);
+        }
       }
-      o[0] = make_float4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
-      o[1] = make_float4(sum[4] * inv, sum[5] * inv, sum[6] * inv, sum[7] * inv);
-      o[32] = make_float4(mx[0], mx[1], mx[2], mx[3]);
-      o[33] = make_float4(mx[4], mx[5], mx[6], mx[7]);
-      o[64] = make_float4(mn[0], mn[1], mn[2], mn[3]);
-      o[65] = make_float4(mn[4], mn[5], mn[6], mn[7]);
     }
+    cur = nxt;
+    tok_cur = tok_nxt;
+    nxt = far;
+    tok_nxt = checked(tok_far);
+    k ^= 1;
   }
-}
-
-// Step 6 with a rotation on the way (sign -1: the transpose, which takes dQ and dK in tile
-// order to raster order and through the rotary positions in one pass).
-template <bool kHalf>
-__global__ void __launch_bounds__(kCopyThreads) rotary_unpermute_kernel(const __grid_constant__ TileArgs p) {
-  const GatherArgs& a = p.g;
-  const uint32_t lane = threadIdx.x & 31;
-  const uint32_t c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-  const Turn<kHalf> turn(static_cast<int32_t>(c), lane, p.P, p.sign);
-  for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-    int32_t b, h, t;
-    unit_coords(u, a.H, a.nT, b, h, t);
-    const int32_t* m = a.map + static_cast<int64_t>(h) * a.Npad + static_cast<int64_t>(t) * 128;
-    const uint8_t* src = a.src + ((static_cast<int64_t>(b) * a.H + h) * a.Npad + static_cast<int64_t>(t) * 128) * kRowBytes;
-    const float2* cs = p.cs + b * p.batch_rows * p.P;
-    int32_t tok[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) tok[i] = __ldg(m + r0 + 16 * i);
-    uint4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (tok[i] >= a.N) flag_status(ST_BAD_MAP);
-      if (tok[i] >= a.N) tok[i] = -1;
-      if (tok[i] >= 0) v[i] = ld_stream(src + (r0 + 16 * i) * kRowBytes + c * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      typename Turn<kHalf>::CosSin t4;
-      turn.load(t4, cs + static_cast<int64_t>(tok[i] < 0 ? 0 : tok[i]) * p.P, tok[i] >= 0);
-      float f[8];
-      turn.apply(v[i], t4, f);
-      if (tok[i] >= 0)
-        st_v4(a.dst + ((static_cast<int64_t>(b) * a.N + tok[i]) * a.H + h) * kRowBytes + c * 16,
-              turn.turned ? Vec<__nv_bfloat16>::put(f) : v[i]);
-    }
-  }
+  copies_wait<0>();
 }
 
 }  // namespace rotary

@@ -34,9 +34,9 @@ struct DeviceInfo {
   int sms = 0;
   bool attrs_set = false;
   int per_sm_copy = 1, per_sm_unpermute = 1, per_sm_pool = 1, per_sm_permpool = 1;   // resident CTAs per SM
-  int per_sm_rotpool[2] = {1, 1}, per_sm_rotback[2] = {1, 1};   // [half layout]
 };
 constexpr int kMaxDevices = 64;
+static_assert(2 * rotary::tile_buffer_bytes(rotary::kTileHeads, 64) <= 48 * 1024, "no opt-in needed");
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 
@@ -90,6 +90,12 @@ veda_status current_device(int& sms) {
         {reinterpret_cast<const void*>(bwd::bwd_kernel<bwd::kModeDKDV>), static_cast<int>(bwd::kSmemBytesDKDV)},
         {reinterpret_cast<const void*>(sgemm::nt_gemm_3xtf32_kernel), static_cast<int>(sgemm::kSmemBytes)},
         {reinterpret_cast<const void*>(select_kernel), static_cast<int>(kSelMaxSmem)},
+        {reinterpret_cast<const void*>(int8::quant_ring_kernel<__nv_bfloat16, true>), 49152},
+        {reinterpret_cast<const void*>(int8::quant_ring_kernel<__half, true>), 49152},
+        {reinterpret_cast<const void*>(int8::quant_ring_kernel<float, true>), 98304},
+        {reinterpret_cast<const void*>(int8::quant_ring_kernel<__nv_bfloat16, false>), 49152},
+        {reinterpret_cast<const void*>(int8::quant_ring_kernel<__half, false>), 49152},
+        {reinterpret_cast<const void*>(int8::quant_ring_kernel<float, false>), 98304},
         {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__nv_bfloat16>), static_cast<int>(int8::kSmemBytes)},
         {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__half>), static_cast<int>(int8::kSmemBytes)},
         {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float>), static_cast<int>(int8::kSmemBytes)},
@@ -117,20 +123,12 @@ veda_status current_device(int& sms) {
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_copy, permute_kernel, kCopyThreads, 0)) != cudaSuccess ||
         (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_unpermute, unpermute_kernel, kCopyThreads, 0)) != cudaSuccess ||
         (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_pool, pool_kernel, kPoolThreads, 0)) != cudaSuccess ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_permpool, permute_pool_kernel, kPoolThreads, 0)) != cudaSuccess ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotpool[0], rotary::rotary_permute_pool_kernel<false>, kPoolThreads, 0)) != cudaSuccess ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotpool[1], rotary::rotary_permute_pool_kernel<true>, kPoolThreads, 0)) != cudaSuccess ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotback[0], rotary::rotary_unpermute_kernel<false>, kCopyThreads, 0)) != cudaSuccess ||
-        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_rotback[1], rotary::rotary_unpermute_kernel<true>, kCopyThreads, 0)) != cudaSuccess)
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_permpool, permute_pool_kernel, kPoolThreads, 0)) != cudaSuccess)
       return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
     d.per_sm_copy = d.per_sm_copy < 1 ? 1 : d.per_sm_copy;
     d.per_sm_unpermute = d.per_sm_unpermute < 1 ? 1 : d.per_sm_unpermute;
     d.per_sm_pool = d.per_sm_pool < 1 ? 1 : d.per_sm_pool;
     d.per_sm_permpool = d.per_sm_permpool < 1 ? 1 : d.per_sm_permpool;
-    for (int i = 0; i < 2; ++i) {
-      d.per_sm_rotpool[i] = std::max(1, d.per_sm_rotpool[i]);
-      d.per_sm_rotback[i] = std::max(1, d.per_sm_rotback[i]);
-    }
     d.attrs_set = true;
   }
   sms = d.sms;
@@ -276,6 +274,40 @@ veda_status check_int8_product(const char* call, const void* a, const float* a_s
     return fail(VEDA_ERR_INVALID_ARG, std::string(call) + ": missing or misaligned buffer");
   if (M > 1 && y_stride < N) return fail(VEDA_ERR_INVALID_ARG, std::string(call) + ": rows of y overlap");
   return VEDA_OK;
+}
+
+// Heads in groups of at most 8, as equal as they come; 24 warps an SM (80 registers a thread).
+veda_status launch_rotary_tiles(rotary::TileArgs& p, bool half_layout, bool gather, int sms, cudaStream_t s) {
+  p.groups = (p.g.H + rotary::kTileHeads - 1) / rotary::kTileHeads;
+  p.hg = (p.g.H + p.groups - 1) / p.groups;
+  p.g.units = static_cast<int64_t>(p.g.B) * p.g.nT * p.groups;
+  const uint32_t bytes = 2 * rotary::tile_buffer_bytes(p.hg, p.P);        // at most 40 KB
+  const int per_sm = std::min(24 / p.hg, static_cast<int>(200 * 1024 / bytes));
+  typedef void (*Kernel)(const rotary::TileArgs);
+  static const Kernel kernels[2][2][2] = {     // [half layout][gather][every channel turned]
+      {{rotary::rotary_tiles_kernel<false, false, false>, rotary::rotary_tiles_kernel<false, false, true>},
+       {rotary::rotary_tiles_kernel<false, true, false>, rotary::rotary_tiles_kernel<false, true, true>}},
+      {{rotary::rotary_tiles_kernel<true, false, false>, rotary::rotary_tiles_kernel<true, false, true>},
+       {rotary::rotary_tiles_kernel<true, true, false>, rotary::rotary_tiles_kernel<true, true, true>}}};
+  kernels[half_layout][gather][p.P == 64]<<<grid_for(p.g.units, sms, per_sm), 32 * p.hg, bytes, s>>>(p);
+  return launched("rotary_tiles_kernel");
+}
+
+// The ring kernels for aligned rows of up to 8,192 values: as many CTAs as stay resident (their
+// rings of 3 rows, at most 96 KB of fp32, and 64 to 96 registers a thread).
+template <typename T>
+void launch_quant(const int8::QuantArgs& a, int sms, cudaStream_t s) {
+  constexpr int kRowUnits = int8::kQuantVecs * 8 * static_cast<int>(sizeof(T)) * int8::kQuantStages;   // bytes a thread
+  if (a.vec && a.kp <= int8::kQuantWarpK) {
+    const int64_t ctas = (a.rows + 7) / 8;
+    int8::quant_ring_kernel<T, true><<<grid_for(ctas, sms, sizeof(T) == 4 ? 2 : 4), 256, 256 * kRowUnits, s>>>(a);
+  } else if (a.vec && a.kp <= int8::kQuantMaxK) {
+    const int threads = ((a.kp + 8 * int8::kQuantVecs - 1) / (8 * int8::kQuantVecs) + 31) / 32 * 32;
+    const int per_sm = std::min(sizeof(T) == 4 ? 512 / threads : 1024 / threads, 8);
+    int8::quant_ring_kernel<T, false><<<grid_for(a.rows, sms, per_sm), threads, threads * kRowUnits, s>>>(a);
+  } else {
+    int8::quant_row_kernel<T><<<grid_for(a.rows, sms, 8), int8::kQuantThreads, 0, s>>>(a);
+  }
 }
 
 template <typename T>
@@ -953,18 +985,12 @@ veda_status veda_rotary_permute_pool(const void* x, void* x_tiled, const float* 
     int sms;
     if ((st = current_device(sms)) != VEDA_OK) return st;
     rotary::TileArgs p{};
-    p.g = {static_cast<const uint8_t*>(x), static_cast<uint8_t*>(x_tiled), tile_map, B, N, H, Npad, Npad / 128,
-           static_cast<int64_t>(B) * H * (Npad / 128)};
+    p.g = {static_cast<const uint8_t*>(x), static_cast<uint8_t*>(x_tiled), tile_map, B, N, H, Npad, Npad / 128, 0};
     p.valid = tile_valid; p.pooled = pooled;
     p.cs = reinterpret_cast<const float2*>(cos_sin);
     p.batch_rows = table_rows == N ? 0 : N;
     p.P = rot_dim / 2; p.sign = 1.f;
-    const int64_t ctas = (p.g.units + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
-    auto* k = interleaved ? rotary::rotary_permute_pool_kernel<false> : rotary::rotary_permute_pool_kernel<true>;
-    const DeviceInfo& d = device_info();
-    k<<<grid_for(ctas, sms, interleaved ? d.per_sm_rotpool[0] : d.per_sm_rotpool[1]), kPoolThreads, 0,
-        reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launched("rotary_permute_pool_kernel");
+    return launch_rotary_tiles(p, interleaved == 0, true, sms, reinterpret_cast<cudaStream_t>(stream));
   });
 }
 
@@ -981,16 +1007,11 @@ veda_status veda_rotary_unpermute(const void* x_tiled, void* x, const float* cos
     int sms;
     if ((st = current_device(sms)) != VEDA_OK) return st;
     rotary::TileArgs p{};
-    p.g = {static_cast<const uint8_t*>(x_tiled), static_cast<uint8_t*>(x), tile_map, B, N, H, Npad, Npad / 128,
-           static_cast<int64_t>(B) * H * (Npad / 128)};
+    p.g = {static_cast<const uint8_t*>(x_tiled), static_cast<uint8_t*>(x), tile_map, B, N, H, Npad, Npad / 128, 0};
     p.cs = reinterpret_cast<const float2*>(cos_sin);
     p.batch_rows = table_rows == N ? 0 : N;
     p.P = rot_dim / 2; p.sign = inverse ? -1.f : 1.f;
-    auto* k = interleaved ? rotary::rotary_unpermute_kernel<false> : rotary::rotary_unpermute_kernel<true>;
-    const DeviceInfo& d = device_info();
-    k<<<grid_for(p.g.units, sms, interleaved ? d.per_sm_rotback[0] : d.per_sm_rotback[1]), kCopyThreads, 0,
-        reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launched("rotary_unpermute_kernel");
+    return launch_rotary_tiles(p, interleaved == 0, false, sms, reinterpret_cast<cudaStream_t>(stream));
   });
 }
 
@@ -1009,17 +1030,9 @@ veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t dtype, v
     int8::QuantArgs a{x, x_stride, static_cast<int8_t*>(codes), scale, rows, K, (K + 15) / 16 * 16,
                       aligned(x, 16) && x_stride * es % 16 == 0 ? 1 : 0};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a.kp <= int8::kQuantWarpK) {
-      const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-      if (dtype == VEDA_BF16) int8::quant_warp_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-      else if (dtype == VEDA_FP16) int8::quant_warp_kernel<__half><<<grid, 256, 0, s>>>(a);
-      else int8::quant_warp_kernel<float><<<grid, 256, 0, s>>>(a);
-    } else {
-      const unsigned grid = static_cast<unsigned>(rows);
-      if (dtype == VEDA_BF16) int8::quant_row_kernel<__nv_bfloat16><<<grid, int8::kQuantThreads, 0, s>>>(a);
-      else if (dtype == VEDA_FP16) int8::quant_row_kernel<__half><<<grid, int8::kQuantThreads, 0, s>>>(a);
-      else int8::quant_row_kernel<float><<<grid, int8::kQuantThreads, 0, s>>>(a);
-    }
+    if (dtype == VEDA_BF16) launch_quant<__nv_bfloat16>(a, sms, s);
+    else if (dtype == VEDA_FP16) launch_quant<__half>(a, sms, s);
+    else launch_quant<float>(a, sms, s);
     return launched("quantize_int8");
   });
 }
