@@ -259,9 +259,9 @@ struct MatArgs {
   int64_t ldo;           // elements
   int32_t M, N, kp;
   int32_t chunks;        // K chunks of 128 codes
-  int32_t tiles_m, tiles_n;
+  int32_t tiles_n;
   int64_t tiles;
-  int32_t out_vec;       // rows of out start on 16-byte boundaries
+  int32_t out_vec;       // every even column of out can be written with its neighbour
 };
 
 __device__ __forceinline__ float scaled(int32_t acc, float sa, float sw, float bias) {
@@ -319,24 +319,36 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const MatArgs p
 }
 
 // ------------------------------------------------------------------------------------
-// The tensor-core product: persistent, one CTA per SM, 128 tokens x 256 channels per tile.
-//   warp 4   TMA producer: per 128-deep K chunk, 128 rows of A and 256 rows of W (128-byte
-//            swizzle) into a kStages-deep ring
-//   warp 5   MMA issuer (one thread): four kind::i8 MMAs (M 128, N 256, K 32) a chunk into one of
-//            two accumulators of 256 TMEM columns
-//   warps 0..3  epilogue: 32 columns at a time, one output row per thread; overlaps the next
-//            tile's main loop
-// Tiles run channel-fastest, so the CTAs of one wave share a few rows of A and all of W from L2.
-// Every wait is bounded; on a timeout the CTA raises its abort flag, the roles leave their loops,
-// in-flight copies and MMAs are drained and the tensor memory is freed.
+// The tensor-core product: persistent pairs of CTAs (clusters of two), 256 tokens x kBN channels a
+// tile. tcgen05.mma with cta_group::2 runs on both SMs of a pair: each CTA loads 128 rows of A and
+// kBN / 2 rows of W a chunk, half of what two separate 128 x kBN tiles would fetch. That is what
+// the pair is for: at kBN = 256 a chunk of 512 tensor cycles needs 64 bytes a cycle and SM from L2
+// (about what 148 SMs get); one CTA alone at 128 x 256 needs 96, and measured 933 us at
+// 50,220 x 5,120 x 5,120.
+//   warp 4 (both CTAs)  TMA producer: per 128-deep K chunk its rows of A and W (128-byte swizzle)
+//            into a kStages-deep ring; the bytes of both CTAs are counted on the leader's barrier
+//   warp 5 (leader)     MMA issuer (one thread): four kind::i8 MMAs (M 256, N kBN, K 32) a chunk into
+//            one of two accumulators; its commits free the stage in both CTAs
+//   warps 0..3 (both)   epilogue of the CTA's 128 rows, 64 columns at a time: accumulators through
+//            shared memory, so that a lane holds two neighbouring columns (their scales and biases
+//            in registers) and every row of the output is written in contiguous pieces whatever its
+//            alignment; overlaps the next tile's main loop
+// Tiles run channel-fastest, so the pairs of one wave share a few rows of A and all of W from L2.
+// Every wait is bounded; on a timeout a CTA raises its abort flag, its roles leave their loops, the
+// other CTA's waits run out in turn, in-flight copies and MMAs are drained, and both meet at the
+// cluster barrier before the tensor memory is freed.
 // ------------------------------------------------------------------------------------
 constexpr int kThreads = 192;
-constexpr int kStages = 4;
-constexpr int kBM = 128, kBN = 256;
-constexpr uint32_t kABytes = kBM * 128, kBBytes = kBN * 128;
-constexpr uint32_t kStageB = kABytes + kBBytes;
-constexpr uint32_t kSmemBytes = kStages * kStageB + 1024;
+constexpr int kBM = 256;                                      // rows per pair
+constexpr uint32_t kStageTotal = 6 * 32768;                   // ring bytes a CTA
+template <int BN> constexpr uint32_t stage_bytes() { return 16384u + static_cast<uint32_t>(BN) * 64u; }
+template <int BN> constexpr int stages() { return static_cast<int>(kStageTotal / stage_bytes<BN>()); }
+constexpr int kMaxStages = 9;
+constexpr uint32_t kEpiStride = 66;                           // words a staged row: pairs free of bank conflicts
+constexpr uint32_t kEpiWarpBytes = 32 * kEpiStride * 4;
+constexpr uint32_t kSmemBytes = kStageTotal + 4 * kEpiWarpBytes + 1024;
 constexpr uint32_t kTmemCols = 512;
+static_assert(stages<64>() <= kMaxStages && stages<128>() <= kMaxStages, "barriers for every stage");
 
 // Instruction descriptor of kind::i8: signed A and B, both K-major, s32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
@@ -344,55 +356,122 @@ __host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// D[tmem of both CTAs] (+)= A B^T over a pair of CTAs; descriptors of the leader's shared memory, the
+// other CTA's operands at the same offsets.
+__device__ __forceinline__ void mma2_ss_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Arrive on `bar` of both CTAs when every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// This CTA's box of a tensor map into its own shared memory, counted on a barrier of the pair.
+__device__ __forceinline__ void tma2_load(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(dst),
+      "l"(map), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait with cluster scope (arrivals of the other CTA's threads).
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
+  if (try_wait_cluster(bar, parity)) return true;
+  if (!mbar_wait_slow(bar, parity, abort, site, kWaitLimitNs)) return false;
+  return try_wait_cluster(bar, parity);            // the phase is complete: this one acquires it
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
 };
 
-// 32 accumulator columns of one output row: scale, bias, store.
+// 32 rows x 64 columns of accumulators, staged in shared memory, to the output: lane l holds columns
+// n0 + 2 l and n0 + 2 l + 1; `sa` is the scale of row m0 + lane.
 template <typename T>
-__device__ __forceinline__ void store32(const MatArgs& p, const uint32_t (&r)[32], int64_t m, int32_t n0, float sa) {
+__device__ __forceinline__ void store_staged(const MatArgs& p, const uint32_t* staged, int32_t m0, int32_t n0, uint32_t lane,
+                                             float sa) {
   using V = rotary::Vec<T>;
-  T* row = static_cast<T*>(p.out) + m * p.ldo;
-  if (p.out_vec && n0 + 32 <= p.N) {
-#pragma unroll
-    for (int j = 0; j < 32; j += V::E) {
-      float f[V::E];
-#pragma unroll
-      for (int i = 0; i < V::E; ++i)
-        f[i] = scaled(static_cast<int32_t>(r[j + i]), sa, __ldg(p.sw + n0 + j + i),
-                      p.bias ? __ldg(p.bias + n0 + j + i) : 0.f);
-      *reinterpret_cast<uint4*>(row + n0 + j) = V::put(f);
+  const int32_t n = n0 + 2 * static_cast<int32_t>(lane);
+  const bool have0 = n < p.N, have1 = n + 1 < p.N;
+  const float w0 = have0 ? __ldg(p.sw + n) : 0.f, w1 = have1 ? __ldg(p.sw + n + 1) : 0.f;
+  const float b0 = p.bias && have0 ? __ldg(p.bias + n) : 0.f, b1 = p.bias && have1 ? __ldg(p.bias + n + 1) : 0.f;
+  const int32_t rows = min(32, p.M - m0);
+  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(m0) * p.ldo + n;
+#pragma unroll 4
+  for (int32_t r = 0; r < rows; ++r, out += p.ldo) {
+    const int2 acc = *reinterpret_cast<const int2*>(staged + r * kEpiStride + 2 * lane);
+    const float s = __shfl_sync(0xffffffffu, sa, r);
+    const float y0 = scaled(acc.x, s, w0, b0), y1 = scaled(acc.y, s, w1, b1);
+    if (p.out_vec) {                          // ldo and the address are even
+      if (have1) {
+        T v[2] = {V::to(y0), V::to(y1)};
+        if (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(v);
+        else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(v);
+        continue;
+      }
+    } else if (have1) {
+      out[1] = V::to(y1);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (n0 + j < p.N)
-        row[n0 + j] = V::to(scaled(static_cast<int32_t>(r[j]), sa, __ldg(p.sw + n0 + j),
-                                   p.bias ? __ldg(p.bias + n0 + j) : 0.f));
+    if (have0) out[0] = V::to(y0);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
                  const __grid_constant__ MatArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ Bars bars;
+  __shared__ __align__(8) Bars bars;
+  constexpr int kStages = stages<BN>();
+  constexpr uint32_t kStageB = stage_bytes<BN>();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
   volatile int* abort = &bars.abort;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -401,70 +480,83 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.acc_full[i]), 1);
-      mbar_init(smem_u32(&bars.acc_empty[i]), 4);
+      mbar_init(smem_u32(&bars.acc_empty[i]), 8);      // the epilogue warps of both CTAs
     }
     mbar_init(smem_u32(&bars.drain), 1);
     bars.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
-    tmem_alloc(smem_u32(&bars.tmem_base), kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 5) tmem_alloc2(smem_u32(&bars.tmem_base), kTmemCols);
   if (warp == 4 && lane == 0) {
     prefetch_tensormap(&mA);
     prefetch_tensormap(&mB);
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                      // both CTAs' barriers and tensor memory exist
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (warp < 4) {
+    uint32_t* staged = reinterpret_cast<uint32_t*>(smem + kStageTotal + warp * kEpiWarpBytes);
     uint32_t it = 0;
-    for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
-      const int32_t m0 = static_cast<int32_t>(t / p.tiles_n) * kBM, n0 = static_cast<int32_t>(t % p.tiles_n) * kBN;
+    for (int64_t t = pair; t < p.tiles; t += pairs, ++it) {
+      const int32_t m0 = static_cast<int32_t>(t / p.tiles_n) * kBM + static_cast<int32_t>(rank * 128 + warp * 32);
+      const int32_t n0 = static_cast<int32_t>(t % p.tiles_n) * BN;
       const uint32_t ab = it & 1;
+      const int32_t m = m0 + static_cast<int32_t>(lane);
+      const float sa = m < p.M ? __ldg(p.sa + m) : 0.f;
       if (!attn::warp_wait_abort(smem_u32(&bars.acc_full[ab]), (it >> 1) & 1, abort, 70)) break;
       tc_fence_after();
-      const int32_t m = m0 + static_cast<int32_t>(warp * 32 + lane);
-      const float sa = m < p.M ? p.sa[m] : 0.f;
-      const uint32_t taddr = tmem + ((warp * 32) << 16) + ab * kBN;
+      const uint32_t taddr = tmem + ((warp * 32) << 16) + ab * 256;
 #pragma unroll 1
-      for (int cc = 0; cc < kBN / 32; ++cc) {
-        if (n0 + cc * 32 >= p.N) break;
-        uint32_t r[32];
-        tmem_ld32_sync(taddr + cc * 32, r);
-        if (m < p.M) store32<T>(p, r, m, n0 + cc * 32, sa);
+      for (int cc = 0; cc < BN; cc += 64) {
+        if (n0 + cc >= p.N || m0 >= p.M) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          tmem_ld32_sync(taddr + cc + 32 * h, r);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            *reinterpret_cast<uint2*>(staged + lane * kEpiStride + 32 * h + j) = make_uint2(r[j], r[j + 1]);
+        }
+        __syncwarp();
+        store_staged<T>(p, staged, m0, n0 + cc, lane, sa);
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.acc_empty[ab]));
+      if (lane == 0) arrive_cluster(map_to_cta(smem_u32(&bars.acc_empty[ab]), 0));
     }
   } else if (warp == 4 && lane == 0) {
     uint32_t g = 0;
-    for (int64_t t = blockIdx.x; t < p.tiles && !*abort; t += gridDim.x) {
-      const int32_t m0 = static_cast<int32_t>(t / p.tiles_n) * kBM, n0 = static_cast<int32_t>(t % p.tiles_n) * kBN;
+    for (int64_t t = pair; t < p.tiles && !*abort; t += pairs) {
+      const int32_t m0 = static_cast<int32_t>(t / p.tiles_n) * kBM + static_cast<int32_t>(rank) * 128;
+      const int32_t n0 = static_cast<int32_t>(t % p.tiles_n) * BN + static_cast<int32_t>(rank) * (BN / 2);
       for (int32_t c = 0; c < p.chunks; ++c, ++g) {
         const uint32_t s = g % kStages;
         if (g >= kStages && !mbar_wait(smem_u32(&bars.empty[s]), (g / kStages - 1) & 1, abort, 71)) {
           t = p.tiles;
           break;
         }
-        const uint32_t st = sb + s * kStageB;
-        mbar_arrive_expect_tx(smem_u32(&bars.full[s]), kStageB);
-        tma_load_2d(st, &mA, smem_u32(&bars.full[s]), c * 128, m0);
-        tma_load_2d(st + kABytes, &mB, smem_u32(&bars.full[s]), c * 128, n0);
+        const uint32_t st = sb + s * kStageB, full = smem_u32(&bars.full[s]);
+        if (rank == 0) mbar_arrive_expect_tx(full, 2 * kStageB);       // both CTAs' bytes
+        const uint32_t leader_full = map_to_cta(full, 0);
+        tma2_load(st, &mA, leader_full, c * 128, m0);
+        tma2_load(st + 16384u, &mB, leader_full, c * 128, n0);
       }
     }
-    for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i)
-      mbar_wait(smem_u32(&bars.full[i % kStages]), (i / kStages) & 1, nullptr, 72);
-  } else if (warp == 5 && lane == 0) {
-    constexpr uint32_t kIdesc = idesc_s8_s32(kBM, kBN);
+    // the leader's barriers count both CTAs' copies: none is in flight when it reaches the cluster barrier
+    if (rank == 0)
+      for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i)
+        mbar_wait(smem_u32(&bars.full[i % kStages]), (i / kStages) & 1, nullptr, 72);
+  } else if (warp == 5 && lane == 0 && rank == 0) {
+    constexpr uint32_t kIdesc = idesc_s8_s32(kBM, BN);
     uint32_t g = 0, it = 0;
-    for (int64_t t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
+    for (int64_t t = pair; t < p.tiles; t += pairs, ++it) {
       const uint32_t ab = it & 1;
-      if (it >= 2 && !mbar_wait(smem_u32(&bars.acc_empty[ab]), ((it >> 1) - 1) & 1, abort, 73)) break;
+      if (it >= 2 && !wait_cluster(smem_u32(&bars.acc_empty[ab]), ((it >> 1) - 1) & 1, abort, 73)) break;
       tc_fence_after();
       bool ok = true;
       for (int32_t c = 0; c < p.chunks; ++c, ++g) {
@@ -475,23 +567,26 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__
         }
         tc_fence_after();
         const uint64_t dA = smem_desc_sw128(sb + s * kStageB, 16, 1024);
-        const uint64_t dB = smem_desc_sw128(sb + s * kStageB + kABytes, 16, 1024);
+        const uint64_t dB = smem_desc_sw128(sb + s * kStageB + 16384u, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)   // 32 codes = 32 bytes per k-step: +2 in 16-byte units
-          mma_ss_i8(tmem + ab * kBN, dA + kk * 2, dB + kk * 2, kIdesc, (c > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&bars.empty[s]));
+          mma2_ss_i8(tmem + ab * 256, dA + kk * 2, dB + kk * 2, kIdesc, (c > 0 || kk > 0) ? 1u : 0u);
+        commit2(smem_u32(&bars.empty[s]));
       }
       if (!ok) break;
-      tc_commit(smem_u32(&bars.acc_full[ab]));
+      commit2(smem_u32(&bars.acc_full[ab]));
     }
-    tc_commit(smem_u32(&bars.drain));
+    commit2(smem_u32(&bars.drain));
     mbar_wait(smem_u32(&bars.drain), 0, nullptr, 75);
+  } else if (warp == 5 && lane == 0) {
+    mbar_wait(smem_u32(&bars.drain), 0, nullptr, 76);  // the leader's last commit has reached this CTA too
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                      // neither CTA's memory is used by the other any more
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 5) tmem_dealloc2(tmem, kTmemCols);
 }
 
 }  // namespace int8

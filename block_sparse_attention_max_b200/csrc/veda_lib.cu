@@ -96,9 +96,15 @@ veda_status current_device(int& sms) {
         {reinterpret_cast<const void*>(int8::quant_ring_kernel<__nv_bfloat16, false>), 49152},
         {reinterpret_cast<const void*>(int8::quant_ring_kernel<__half, false>), 49152},
         {reinterpret_cast<const void*>(int8::quant_ring_kernel<float, false>), 98304},
-        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__nv_bfloat16>), static_cast<int>(int8::kSmemBytes)},
-        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__half>), static_cast<int>(int8::kSmemBytes)},
-        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__nv_bfloat16, 64>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__nv_bfloat16, 128>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__nv_bfloat16, 256>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__half, 64>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__half, 128>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<__half, 256>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float, 64>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float, 128>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float, 256>), static_cast<int>(int8::kSmemBytes)},
     };
     for (auto& x : attrs) {
       e = cudaFuncSetAttribute(x.f, cudaFuncAttributeMaxDynamicSharedMemorySize, x.bytes);
@@ -322,11 +328,26 @@ veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
   }
   veda_status st = get_encoder();
   if (st != VEDA_OK) return st;
+  // Channels per tile: the width that ends first. A chunk of 128 codes costs a pair the slower of its
+  // tensor cycles (2 BN) and its copies from L2 (128 + BN / 2 rows of 128 bytes at 64 bytes a cycle).
+  const int64_t pairs = sms / 2;
+  int bn = 256;
+  int64_t best = INT64_MAX;
+  for (const int w : {256, 128, 64}) {
+    const int64_t tiles = static_cast<int64_t>((p.M - 1) / int8::kBM + 1) * ((p.N - 1) / w + 1);
+    const int64_t chunk = std::max(2 * w, 2 * (128 + w / 2)), cost = ((tiles + pairs - 1) / pairs) * (p.chunks * chunk + 2000 + 8 * w);
+    if (cost < best) {
+      best = cost;
+      bn = w;
+    }
+  }
+  p.tiles_n = (p.N - 1) / bn + 1;
+  p.tiles = static_cast<int64_t>((p.M - 1) / int8::kBM + 1) * p.tiles_n;
   CUtensorMap mA, mB;
-  if ((st = encode_codes(mA, p.a, p.kp, p.M, int8::kBM)) != VEDA_OK ||
-      (st = encode_codes(mB, p.w, p.kp, p.N, int8::kBN)) != VEDA_OK)
+  if ((st = encode_codes(mA, p.a, p.kp, p.M, 128)) != VEDA_OK || (st = encode_codes(mB, p.w, p.kp, p.N, bn / 2)) != VEDA_OK)
     return st;
-  int8::int8_gemm_kernel<T><<<grid_for(p.tiles, sms, 1), int8::kThreads, int8::kSmemBytes, s>>>(mA, mB, p);
+  auto* k = bn == 256 ? int8::int8_gemm_kernel<T, 256> : bn == 128 ? int8::int8_gemm_kernel<T, 128> : int8::int8_gemm_kernel<T, 64>;
+  k<<<2 * grid_for(p.tiles, static_cast<int>(pairs), 1), int8::kThreads, int8::kSmemBytes, s>>>(mA, mB, p);
   return launched("int8_gemm_kernel");
 }
 }  // namespace
@@ -1056,9 +1077,7 @@ veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w,
     p.out = y; p.ldo = y_stride;
     p.M = M; p.N = N; p.kp = (K + 15) / 16 * 16;
     p.chunks = (p.kp + 127) / 128;
-    p.tiles_m = (M - 1) / int8::kBM + 1; p.tiles_n = (N - 1) / int8::kBN + 1;
-    p.tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-    p.out_vec = aligned(y, 16) && y_stride * es % 16 == 0;
+    p.out_vec = aligned(y, 2 * es) && y_stride % 2 == 0;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == VEDA_BF16) return launch_int8<__nv_bfloat16>(p, sms, s);
     if (dtype == VEDA_FP16) return launch_int8<__half>(p, sms, s);
