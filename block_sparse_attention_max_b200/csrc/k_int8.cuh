@@ -24,8 +24,7 @@ namespace int8 {
 // values belongs to a group of threads -- a warp up to 1,024 values, a CTA above -- whose thread i
 // owns the 8-value vectors i, i + threads, ...: rows run through a ring of kQuantStages rows in
 // shared memory that each thread fills for itself with asynchronous copies, so the next rows are
-// on their way while one is rounded. Longer rows, and rows that start on no 16-byte boundary, are
-// read twice with plain loads.
+// on their way while one is rounded.
 // The division is exact: x * (1 / scale) is rounded, and where that product lies next to a half the
 // sign of the exactly rounded x - scale (q +- 1/2) decides, ties to even.
 // A row with a NaN or an infinity gets scale NaN (and codes 0), so its outputs are NaN; a row
@@ -46,21 +45,6 @@ constexpr int kQuantMaxK = 8192;      // ring kernels
 constexpr int kQuantVecs = 4;         // vectors a thread
 constexpr int kQuantThreads = 256;    // most threads of a CTA
 constexpr int kQuantStages = 3;
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int32_t k0, int32_t K, bool vec, float* f) {
-  using V = rotary::Vec<T>;
-  if (vec && k0 + 8 <= K) {
-#pragma unroll
-    for (int u = 0; u < 8 / V::E; ++u) {
-      uint4 v = *reinterpret_cast<const uint4*>(row + k0 + u * V::E);
-      V::get(v, f + u * V::E);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = k0 + i < K ? V::one(row[k0 + i]) : 0.f;
-  }
-}
 
 // x / s to the nearest integer, ties to even, |x| <= 127.5 s, for a quotient near a half-integer
 // (x * inv is off by less than 2^-15): fma rounds x - s (q +- 1/2) once, so its sign is exact.
@@ -220,28 +204,60 @@ __global__ void __launch_bounds__(kQuantThreads) quant_ring_kernel(const QuantAr
   rotary::copies_wait<0>();
 }
 
-// Any row: a CTA reads it twice.
+// Rows without 16-byte boundaries, and long ones: a CTA per row, a thread's elements 256 apart, so
+// that every access of a warp is one contiguous piece; the first kQuantHeld of a thread's elements
+// stay in registers between the maximum and the rounding, the rest are read again.
+constexpr int kQuantHeld = 32;
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) quant_row_kernel(const QuantArgs a) {
+  using V = rotary::Vec<T>;
   __shared__ uint32_t red[kQuantThreads / 32];
+  const int32_t me = threadIdx.x;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    T held[kQuantHeld];
+#pragma unroll
+    for (int i = 0; i < kQuantHeld; ++i) {
+      const int32_t k = me + i * kQuantThreads;
+      held[i] = k < a.K ? x[k] : V::to(0.f);
+    }
     uint32_t m = 0;
-    for (int32_t k = threadIdx.x; k < a.K; k += blockDim.x) m = max(m, abs_bits(rotary::Vec<T>::one(x[k])));
+#pragma unroll
+    for (int i = 0; i < kQuantHeld; ++i) m = max(m, abs_bits(V::one(held[i])));
+#pragma unroll 4
+    for (int32_t k = me + kQuantHeld * kQuantThreads; k < a.K; k += kQuantThreads) m = max(m, abs_bits(V::one(x[k])));
     m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    if ((me & 31) == 0) red[me >> 5] = m;
     __syncthreads();
-    for (int32_t w = 0; w < static_cast<int32_t>(blockDim.x >> 5); ++w) m = max(m, red[w]);
+#pragma unroll
+    for (int32_t w = 0; w < kQuantThreads / 32; ++w) m = max(m, red[w]);
     bool live;
     const float s = row_scale(m, live);
     const float inv = 1.0f / s;
     int8_t* out = a.codes + row * a.kp;
-    for (int32_t k0 = threadIdx.x * 8; k0 < a.kp; k0 += blockDim.x * 8) {
+    const auto put8 = [&](const float* f, int32_t k0) {
+      const uint2 q = codes8(f, s, inv, live);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int32_t k = k0 + i * kQuantThreads;
+        if (k < a.kp) out[k] = static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kQuantHeld; j += 8) {
+      if (me + j * kQuantThreads >= a.kp) break;
       float f[8];
-      load8<T>(x, k0, a.K, a.vec != 0, f);
-      *reinterpret_cast<uint2*>(out + k0) = codes8(f, s, inv, live);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = V::one(held[j + i]);
+      put8(f, me + j * kQuantThreads);
     }
-    if (threadIdx.x == 0) a.scale[row] = s;
+    for (int32_t k0 = me + kQuantHeld * kQuantThreads; k0 < a.kp; k0 += 8 * kQuantThreads) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = k0 + i * kQuantThreads < a.K ? V::one(x[k0 + i * kQuantThreads]) : 0.f;
+      put8(f, k0);
+    }
+    if (me == 0) a.scale[row] = s;
     __syncthreads();                                           // red is read before the next row's maxima
   }
 }
@@ -268,53 +284,124 @@ __device__ __forceinline__ float scaled(int32_t acc, float sa, float sw, float b
   return fmaf(static_cast<float>(acc), sa * sw, bias);
 }
 
+// Eight values of row m of x from k0, zeros behind K (the fused form's x has the output's type).
+template <typename T>
+__device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t k0, float* f) {
+  using V = rotary::Vec<T>;
+  const T* x = static_cast<const T*>(q.x) + m * q.x_stride;
+  if (q.vec && k0 + 8 <= q.K) {
+#pragma unroll
+    for (int u = 0; u < 8 / V::E; ++u) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k0) + u);
+      V::get(v, f + u * V::E);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = k0 + i < q.K ? V::one(x[k0 + i]) : 0.f;
+  }
+}
+
 // ------------------------------------------------------------------------------------
 // Few tokens (M <= kFewMax): the weights are read once and that is the whole cost, so a warp
-// takes one output channel's row, 16 bytes a lane with several loads in flight, and forms the
-// products of all tokens with four-way integer dot products (tokens' codes come through L1).
+// takes one output channel's row at a time, 16 bytes a lane with several loads in flight, and forms
+// the products of all tokens with four-way integer dot products. The tokens' codes come from global
+// memory (through L1) or, kFused, are made here: every CTA rounds the few rows of x into its shared
+// memory, while its first weights are already on their way. For one token of 5,120 values that is
+// 10 KB a CTA and saves the separate launch; M x K is bounded (kFewFused) so that it stays small
+// beside the weights.
 // ------------------------------------------------------------------------------------
 constexpr int kFewMax = 8;
 constexpr int kFewThreads = 256;
+constexpr int kFewFused = 16384;      // M * kp of the fused form
 
-template <typename T, int MT>
-__global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const MatArgs p) {
+template <typename T, int MT, bool kFused>
+__global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_constant__ MatArgs p,
+                                                                const __grid_constant__ QuantArgs q) {
   using V = rotary::Vec<T>;
+  extern __shared__ __align__(16) int8_t few_codes[];          // kFused: [M][kp]
+  __shared__ uint32_t few_max[MT];
   const int32_t lane = threadIdx.x & 31;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + (threadIdx.x >> 5);
-  if (n >= p.N) return;
-  const int4* w = reinterpret_cast<const int4*>(p.w + n * p.kp);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
+  int64_t n = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + (threadIdx.x >> 5);
   const int32_t vecs = p.kp / 16;
-  int32_t acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = 0;
   constexpr int U = 4;
-  for (int32_t v0 = lane; v0 < vecs; v0 += 32 * U) {
-    int4 wv[U];
+  int4 wv[U];
+  const auto load = [&](int64_t channel, int32_t v0) {
+    const int4* w = reinterpret_cast<const int4*>(p.w + channel * p.kp);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       wv[u] = make_int4(0, 0, 0, 0);
-      if (v0 + 32 * u < vecs) wv[u] = __ldcs(w + v0 + 32 * u);
+      if (channel < p.N && v0 + 32 * u < vecs) wv[u] = __ldcs(w + v0 + 32 * u);
     }
+  };
+  load(n, lane);
+  float sa[MT];
+  if constexpr (kFused) {
+    if (threadIdx.x < MT) few_max[threadIdx.x] = 0u;
+    __syncthreads();
+    for (int32_t m = 0; m < p.M; ++m) {
+      uint32_t big = 0;
+      for (int32_t k0 = threadIdx.x * 8; k0 < p.kp; k0 += kFewThreads * 8) {
+        float f[8];
+        few_load<T>(q, m, k0, f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (v0 + 32 * u >= vecs) continue;
+        for (int i = 0; i < 8; ++i) big = max(big, abs_bits(f[i]));
+      }
+      big = __reduce_max_sync(0xffffffffu, big);
+      if (lane == 0) atomicMax(&few_max[m], big);
+    }
+    __syncthreads();
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (m >= p.M) continue;
-        const int4 av = __ldg(reinterpret_cast<const int4*>(p.a + static_cast<int64_t>(m) * p.kp) + v0 + 32 * u);
-        acc[m] = __dp4a(wv[u].x, av.x, acc[m]);
-        acc[m] = __dp4a(wv[u].y, av.y, acc[m]);
-        acc[m] = __dp4a(wv[u].z, av.z, acc[m]);
-        acc[m] = __dp4a(wv[u].w, av.w, acc[m]);
+    for (int m = 0; m < MT; ++m) {
+      if (m >= p.M) continue;
+      bool live;
+      sa[m] = row_scale(few_max[m], live);
+      const float inv = 1.0f / sa[m];
+      for (int32_t k0 = threadIdx.x * 8; k0 < p.kp; k0 += kFewThreads * 8) {
+        float f[8];
+        few_load<T>(q, m, k0, f);
+        *reinterpret_cast<uint2*>(few_codes + m * p.kp + k0) = codes8(f, sa[m], inv, live);
       }
     }
-  }
-  const float sw = p.sw[n], bias = p.bias ? p.bias[n] : 0.f;
+    __syncthreads();
+  } else {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    if (m >= p.M) continue;
-    const int32_t s = __reduce_add_sync(0xffffffffu, acc[m]);
-    if (lane == m) static_cast<T*>(p.out)[m * p.ldo + n] = V::to(scaled(s, p.sa[m], sw, bias));
+    for (int m = 0; m < MT; ++m) sa[m] = m < p.M ? __ldg(p.sa + m) : 0.f;
+  }
+  for (; n < p.N; n += step) {
+    const float sw = __ldg(p.sw + n), bias = p.bias ? __ldg(p.bias + n) : 0.f;
+    int32_t acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = 0;
+    for (int32_t v0 = lane; v0 < vecs; v0 += 32 * U) {
+      int4 cur[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = wv[u];
+      // the next weights of this channel, or the first of the warp's next one
+      if (v0 + 32 * U < vecs) load(n, v0 + 32 * U);
+      else load(n + step, lane);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (v0 + 32 * u >= vecs) continue;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m >= p.M) continue;
+          const int4 av = kFused ? *(reinterpret_cast<const int4*>(few_codes + m * p.kp) + v0 + 32 * u)
+                                 : __ldg(reinterpret_cast<const int4*>(p.a + static_cast<int64_t>(m) * p.kp) + v0 + 32 * u);
+          acc[m] = __dp4a(cur[u].x, av.x, acc[m]);
+          acc[m] = __dp4a(cur[u].y, av.y, acc[m]);
+          acc[m] = __dp4a(cur[u].z, av.z, acc[m]);
+          acc[m] = __dp4a(cur[u].w, av.w, acc[m]);
+        }
+      }
+    }
+    if (lane >= vecs) load(n + step, lane);      // a lane that owns no vector of a short row
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (m >= p.M) continue;
+      const int32_t s = __reduce_add_sync(0xffffffffu, acc[m]);
+      if (lane == m) static_cast<T*>(p.out)[m * p.ldo + n] = V::to(scaled(s, sa[m], sw, bias));
+    }
   }
 }
 

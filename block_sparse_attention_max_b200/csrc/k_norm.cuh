@@ -321,11 +321,11 @@ __device__ __forceinline__ Slice slice_of(const Args& a) {
 }
 
 // ------------------------------------------------------------------------------------
-// Forward. TI: type of x; TO: type of y and of the residual. 64 registers, so that two CTAs of
-// 512 threads (three of 320) share an SM and one's barriers hide behind the other's work.
+// Forward. TI: type of x; TO: type of y and of the residual. At least two CTAs share an SM, so that
+// one's barriers hide behind the other's work (64 registers at 512 threads, 128 at 256).
 // ------------------------------------------------------------------------------------
 template <typename TI, typename TO, int NV, bool kWarp, bool kAligned>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kMaxThreads, 2)
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : NV == 4 ? 256 : kMaxThreads, 2)
 norm_fwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
   __shared__ __align__(16) float red[2][1][kMaxWarps];
@@ -475,7 +475,7 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
 // kBound: most threads of the CTA; 320 (up to 5,120 channels) leaves room for two CTAs an SM.
 // ------------------------------------------------------------------------------------
 template <typename TI, typename TO, int NV, bool kWarp, int kBound, bool kAligned>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kBound, kBound == kMaxThreads || (kWarp && NV == 4) ? 1 : 2)
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kBound, (kBound == kMaxThreads && NV > 1) || (kWarp && NV == 4) ? 1 : 2)
 norm_bwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
   __shared__ __align__(16) float red[2][2][kMaxWarps];

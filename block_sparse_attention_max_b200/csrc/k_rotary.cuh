@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 // bytes of the row it turns. Read by every head from L2, 8 to 16 rows in registers at a time, the
 // gather of the 16:9 clip took 378 us a tensor. Neighbouring heads mostly have the same tile map,
 // so the CTA copies the rows of its first head's tokens once; a warp whose head has another token
-// in that slot (per-head tile orders) reads that row of the table from global memory instead.
+// in some slot (per-head tile orders) reads its rows of the table from global memory instead.
 //
 // A half warp turns one token row; a lane holds two pieces of four channels, chosen so that both
 // halves of a pair are its own and that a warp's accesses of row and table are contiguous:
@@ -536,41 +536,44 @@ __global__ void __launch_bounds__(32 * kTileHeads, 3) rotary_tiles_kernel(const 
           }
         }
       } else {
-#pragma unroll 1
-        for (int i = 0; i < kBatchRows / 2; ++i) {
-          const int32_t r = 2 * i + half;
-          const int32_t tk = __shfl_sync(0xffffffffu, tok_cur, r), lead = __shfl_sync(0xffffffffu, tok_cur, 16 + r);
-          float g[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] = 0.f;
-          uint2 v1 = make_uint2(0, 0), v2 = v1;
-          if (tk >= 0) {
-            float4 ca, cb;
-            if (tk == lead) {
-              ca = ld_shared_f4(row1 + i * 16 * P);
-              cb = ld_shared_f4(row2 + i * 16 * P);
-            } else {
-              const float2* row = cs + static_cast<int64_t>(tk) * P;
-              ca = __ldg(reinterpret_cast<const float4*>(row + p1));
-              cb = __ldg(reinterpret_cast<const float4*>(row + p2));
-            }
-            turn_row(i, ca, cb, g, v1, v2);
+        for (int i0 = 0; i0 < kBatchRows / 2; i0 += 2) {   // the table's rows of two slots in flight
+          int32_t tk[2];
+          float4 ca[2], cb[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tk[i] = __shfl_sync(0xffffffffu, tok_cur, 2 * (i0 + i) + half);
+            const float2* row = cs + static_cast<int64_t>(max(tk[i], 0)) * P;
+            ca[i] = __ldg(reinterpret_cast<const float4*>(row + p1));
+            cb[i] = __ldg(reinterpret_cast<const float4*>(row + p2));
           }
-          if (kGather) {
-            st_v2(tile1 + 2 * i * kRowBytes, v1);
-            st_v2(tile2 + 2 * i * kRowBytes, v2);
-            if (cur.r0 + r < nv) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                sum[e] += g[e];
-                mx[e] = fmaxf(mx[e], g[e]);
-                mn[e] = fminf(mn[e], g[e]);
-              }
+          for (int i = 0; i < 2; ++i) {
+            const int32_t r = 2 * (i0 + i) + half;
+            float g[8];
+            uint2 v1, v2;
+            turn_row(i0 + i, ca[i], cb[i], g, v1, v2);
+            if (tk[i] < 0) {               // no token: the buffer holds nothing
+#pragma unroll
+              for (int e = 0; e < 8; ++e) g[e] = 0.f;
+              v1 = v2 = make_uint2(0, 0);
             }
-          } else if (tk >= 0) {
-            uint8_t* dst = raster + tk * token_bytes;
-            st_v2(dst + o1 * 2, v1);
-            st_v2(dst + o2 * 2, v2);
+            if (kGather) {
+              st_v2(tile1 + 2 * (i0 + i) * kRowBytes, v1);
+              st_v2(tile2 + 2 * (i0 + i) * kRowBytes, v2);
+              if (cur.r0 + r < nv) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  sum[e] += g[e];
+                  mx[e] = fmaxf(mx[e], g[e]);
+                  mn[e] = fminf(mn[e], g[e]);
+                }
+              }
+            } else if (tk[i] >= 0) {
+              uint8_t* dst = raster + tk[i] * token_bytes;
+              st_v2(dst + o1 * 2, v1);
+              st_v2(dst + o2 * 2, v2);
+            }
           }
         }
       }

@@ -316,16 +316,22 @@ void launch_quant(const int8::QuantArgs& a, int sms, cudaStream_t s) {
   }
 }
 
+// Few tokens; q null: from codes, else from x in the output's type.
+template <typename T, bool kFused>
+veda_status launch_few(const int8::MatArgs& p, const int8::QuantArgs& q, int sms, cudaStream_t s) {
+  // up to 8 CTAs an SM: a warp's next channel follows its last, so that its loads never pause
+  const unsigned grid = grid_for((p.N + int8::kFewThreads / 32 - 1) / (int8::kFewThreads / 32), sms, 6);
+  const size_t smem = kFused ? static_cast<size_t>(p.M) * p.kp : 0;
+  if (p.M == 1) int8::few_tokens_kernel<T, 1, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
+  else if (p.M == 2) int8::few_tokens_kernel<T, 2, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
+  else if (p.M <= 4) int8::few_tokens_kernel<T, 4, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
+  else int8::few_tokens_kernel<T, 8, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
+  return launched("few_tokens_kernel");
+}
+
 template <typename T>
 veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
-  if (p.M <= int8::kFewMax) {
-    const unsigned grid = static_cast<unsigned>((p.N + int8::kFewThreads / 32 - 1) / (int8::kFewThreads / 32));
-    if (p.M == 1) int8::few_tokens_kernel<T, 1><<<grid, int8::kFewThreads, 0, s>>>(p);
-    else if (p.M == 2) int8::few_tokens_kernel<T, 2><<<grid, int8::kFewThreads, 0, s>>>(p);
-    else if (p.M <= 4) int8::few_tokens_kernel<T, 4><<<grid, int8::kFewThreads, 0, s>>>(p);
-    else int8::few_tokens_kernel<T, 8><<<grid, int8::kFewThreads, 0, s>>>(p);
-    return launched("few_tokens_kernel");
-  }
+  if (p.M <= int8::kFewMax) return launch_few<T, false>(p, int8::QuantArgs{}, sms, s);
   veda_status st = get_encoder();
   if (st != VEDA_OK) return st;
   // Channels per tile: the width that ends first. A chunk of 128 codes costs a pair the slower of its
@@ -1105,6 +1111,23 @@ veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, c
     float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + static_cast<size_t>(M) * kp);
     veda_status st = check_int8_product("veda_int8_linear", workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N);
     if (st != VEDA_OK) return st;
+    const int64_t es = type_size(x_dtype);
+    if (M <= int8::kFewMax && static_cast<int64_t>(M) * static_cast<int64_t>(kp) <= int8::kFewFused && x_dtype == y_dtype) {
+      if (!x || !aligned(x, es)) return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: missing or misaligned buffer");
+      int sms;
+      if ((st = current_device(sms)) != VEDA_OK) return st;
+      int8::MatArgs p{};
+      p.w = static_cast<const int8_t*>(w);
+      p.sw = w_scale; p.bias = bias; p.out = y; p.ldo = y_stride;
+      p.M = M; p.N = N; p.kp = static_cast<int32_t>(kp);
+      int8::QuantArgs q{};
+      q.x = x; q.x_stride = x_stride; q.K = K; q.kp = p.kp;
+      q.vec = aligned(x, 16) && (M == 1 || x_stride * es % 16 == 0);
+      const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+      if (y_dtype == VEDA_BF16) return launch_few<__nv_bfloat16, true>(p, q, sms, cs);
+      if (y_dtype == VEDA_FP16) return launch_few<__half, true>(p, q, sms, cs);
+      return launch_few<float, true>(p, q, sms, cs);
+    }
     if ((st = veda_quantize_int8(x, x_stride, x_dtype, workspace, scale, M, K, stream)) != VEDA_OK) return st;
     return veda_int8_matmul(workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N, K, stream);
   });

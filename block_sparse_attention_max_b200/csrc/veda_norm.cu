@@ -39,17 +39,28 @@ bool vec_rows(const void* p, int64_t sb, int64_t sn, int32_t dtype) {
 constexpr int kFwdStages = 4, kBwdStages = 3;
 constexpr int kMaxRing = 224 * 1024;
 
+// Who holds a row. Measured on 120 M bf16 values (share of the HBM copy rate; forward without /
+// with a residual, backward):
+//   a warp, 2 or 4 vectors a lane, up to 1,024 channels: 1,024 channels 79 / 83 / 75%, a CTA of
+//     1-vector threads there 58 / 84 / 63%;
+//   above, a CTA: the row sums cost a thread the same whatever it holds, so more vectors a thread
+//     are faster as long as their registers leave two CTAs an SM: forward without a residual 4
+//     (5,120: 78%; 2: 72%), with one 2 (8,192: 89%; 4: 78%), backward 2 (5,120: 80%; 4: 60%).
+// Rows without 16-byte boundaries are fetched with plain loads that stall their warp, so there more
+// warps with less each are faster: above 256 channels a CTA of 1-vector threads (backward of 6,147
+// rows of 1,023: 29 us; a warp a row 41 us).
 struct Shape {
   int nv;          // vectors per thread
   bool warp;       // a row per warp
   int threads;     // per CTA
 };
-Shape shape_of(int32_t C) {
+Shape shape_of(int32_t C, bool is_aligned, bool bwd, bool res) {
   const int vecs = (C + norm::kVec - 1) / norm::kVec;
-  if (C <= 256) return {1, true, 32 * norm::kWarpsPerCta};
-  if (C <= 512) return {2, true, 32 * norm::kWarpsPerCta};
-  if (C <= norm::kWarpCols) return {4, true, 32 * norm::kWarpsPerCta};
-  return {2, false, ((vecs + 1) / 2 + 31) / 32 * 32};     // at most kMaxThreads
+  const int warp_threads = 32 * norm::kWarpsPerCta;
+  if (C <= 256) return {1, true, warp_threads};
+  if (is_aligned && C <= norm::kWarpCols) return {C <= 512 ? 2 : 4, true, warp_threads};
+  const int nv = is_aligned ? (bwd || res ? 2 : 4) : C <= 4096 ? 1 : 2;
+  return {nv, false, ((vecs + nv - 1) / nv + 31) / 32 * 32};     // at most kMaxThreads (nv 4: 256)
 }
 
 typedef void (*Kernel)(const Args);
@@ -59,7 +70,7 @@ template <int NV, bool W, int BOUND, bool A>
 Kernel pick_types(bool bwd, int32_t ti, int32_t to) {
   using B = __nv_bfloat16;
   using H = __half;
-#define VEDA_PAIR(TI, TO) (bwd ? norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, A> : norm::norm_fwd_kernel<TI, TO, NV, W, A>)
+#define VEDA_PAIR(TI, TO) (bwd ? norm::norm_bwd_kernel<TI, TO, (W ? NV : NV < 2 ? 1 : 2), W, BOUND, A> : norm::norm_fwd_kernel<TI, TO, NV, W, A>)
   if (ti == VEDA_BF16 && to == VEDA_BF16) return VEDA_PAIR(B, B);
   if (ti == VEDA_FP16 && to == VEDA_FP16) return VEDA_PAIR(H, H);
   if (ti == VEDA_FP32 && to == VEDA_FP32) return VEDA_PAIR(float, float);
@@ -75,6 +86,8 @@ Kernel pick_shape(const Shape& s, bool bwd, int32_t ti, int32_t to) {
     if (s.nv == 2) return pick_types<2, true, 256, A>(bwd, ti, to);
     return pick_types<4, true, 256, A>(bwd, ti, to);
   }
+  if (s.nv == 1) return pick_types<1, false, norm::kMaxThreads, A>(bwd, ti, to);
+  if (s.nv == 4) return pick_types<4, false, 320, A>(bwd, ti, to);          // forward only
   return s.threads <= 320 ? pick_types<2, false, 320, A>(bwd, ti, to)
                           : pick_types<2, false, norm::kMaxThreads, A>(bwd, ti, to);
 }
@@ -197,7 +210,7 @@ veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const v
     a.B = B; a.N = N; a.kind = kind;
     const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.y, a.yb, a.yn, y->dtype) &&
             (!residual || vec_rows(a.res, a.rb, a.rn, y->dtype));
-    const Shape s = shape_of(C);
+    const Shape s = shape_of(C, vec, false, residual != nullptr);
     const int bytes = ring_bytes(s, false, x->dtype, y->dtype, residual != nullptr, a.stages);
     const Kernel k = pick(s, false, vec, x->dtype, y->dtype);
     if ((st = slices_for(k, s, bytes, sms, kMaxPerSmFwd, B, N, a.slices)) != VEDA_OK) return st;
@@ -263,7 +276,7 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     a.B = B; a.N = N; a.kind = kind;
     const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.dy, a.db, a.dn, dy->dtype) &&
             vec_rows(a.y, a.yb, a.yn, x->dtype) && (!a.res || vec_rows(a.res, a.rb, a.rn, x->dtype));
-    const Shape s = shape_of(C);
+    const Shape s = shape_of(C, vec, true, a.res != nullptr);
     const int bytes = ring_bytes(s, true, x->dtype, dy->dtype, a.res != nullptr, a.stages);
     a.part = static_cast<float*>(workspace);
     const Kernel k = pick(s, true, vec, x->dtype, dy->dtype);
