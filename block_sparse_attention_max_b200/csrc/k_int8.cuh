@@ -38,6 +38,7 @@ struct QuantArgs {
   int64_t rows;
   int32_t K, kp;
   int32_t vec;           // rows start on 16-byte boundaries
+  int32_t dtype;         // of x (few-token product)
 };
 
 constexpr int kQuantWarpK = 1024;
@@ -284,9 +285,9 @@ __device__ __forceinline__ float scaled(int32_t acc, float sa, float sw, float b
   return fmaf(static_cast<float>(acc), sa * sw, bias);
 }
 
-// Eight values of row m of x from k0, zeros behind K (the fused form's x has the output's type).
+// Eight values of row m of x from k0, zeros behind K.
 template <typename T>
-__device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t k0, float* f) {
+__device__ __forceinline__ void few_load_as(const QuantArgs& q, int32_t m, int32_t k0, float* f) {
   using V = rotary::Vec<T>;
   const T* x = static_cast<const T*>(q.x) + m * q.x_stride;
   if (q.vec && k0 + 8 <= q.K) {
@@ -299,6 +300,11 @@ __device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t 
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = k0 + i < q.K ? V::one(x[k0 + i]) : 0.f;
   }
+}
+__device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t k0, float* f) {
+  if (q.dtype == 0) few_load_as<__nv_bfloat16>(q, m, k0, f);        // VEDA_BF16
+  else if (q.dtype == 1) few_load_as<__half>(q, m, k0, f);          // VEDA_FP16
+  else few_load_as<float>(q, m, k0, f);
 }
 
 // ------------------------------------------------------------------------------------
@@ -313,9 +319,12 @@ __device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t 
 constexpr int kFewMax = 8;
 constexpr int kFewThreads = 256;
 constexpr int kFewFused = 16384;      // M * kp of the fused form
+// CTAs an SM, by the registers of MT tokens; the grid is that many, so that a warp's next channel
+// follows its last and its loads never pause
+template <int MT> constexpr int few_ctas() { return MT <= 2 ? 5 : MT == 4 ? 4 : 3; }
 
 template <typename T, int MT, bool kFused>
-__global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_constant__ MatArgs p,
+__global__ void __launch_bounds__(kFewThreads, few_ctas<MT>()) few_tokens_kernel(const __grid_constant__ MatArgs p,
                                                                 const __grid_constant__ QuantArgs q) {
   using V = rotary::Vec<T>;
   extern __shared__ __align__(16) int8_t few_codes[];          // kFused: [M][kp]
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       uint32_t big = 0;
       for (int32_t k0 = threadIdx.x * 8; k0 < p.kp; k0 += kFewThreads * 8) {
         float f[8];
-        few_load<T>(q, m, k0, f);
+        few_load(q, m, k0, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) big = max(big, abs_bits(f[i]));
       }
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kFewThreads) few_tokens_kernel(const __grid_co
       const float inv = 1.0f / sa[m];
       for (int32_t k0 = threadIdx.x * 8; k0 < p.kp; k0 += kFewThreads * 8) {
         float f[8];
-        few_load<T>(q, m, k0, f);
+        few_load(q, m, k0, f);
         *reinterpret_cast<uint2*>(few_codes + m * p.kp + k0) = codes8(f, sa[m], inv, live);
       }
     }

@@ -316,18 +316,23 @@ void launch_quant(const int8::QuantArgs& a, int sms, cudaStream_t s) {
   }
 }
 
-// Few tokens; q null: from codes, else from x in the output's type.
-template <typename T, bool kFused>
-veda_status launch_few(const int8::MatArgs& p, const int8::QuantArgs& q, int sms, cudaStream_t s) {
-  // up to 8 CTAs an SM: a warp's next channel follows its last, so that its loads never pause
-  const unsigned grid = grid_for((p.N + int8::kFewThreads / 32 - 1) / (int8::kFewThreads / 32), sms, 6);
-  const size_t smem = kFused ? static_cast<size_t>(p.M) * p.kp : 0;
-  if (p.M == 1) int8::few_tokens_kernel<T, 1, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
-  else if (p.M == 2) int8::few_tokens_kernel<T, 2, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
-  else if (p.M <= 4) int8::few_tokens_kernel<T, 4, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
-  else int8::few_tokens_kernel<T, 8, kFused><<<grid, int8::kFewThreads, smem, s>>>(p, q);
+// Few tokens, from codes or (kFused) from the rows of x.
+template <typename T, int MT, bool kFused>
+veda_status launch_few_as(const int8::MatArgs& p, const int8::QuantArgs& q, int sms, cudaStream_t s) {
+  constexpr int kWarps = int8::kFewThreads / 32;
+  int8::few_tokens_kernel<T, MT, kFused><<<grid_for((static_cast<int64_t>(p.N) + kWarps - 1) / kWarps, sms, int8::few_ctas<MT>()),
+                                           int8::kFewThreads, kFused ? static_cast<size_t>(p.M) * p.kp : 0, s>>>(p, q);
   return launched("few_tokens_kernel");
 }
+template <typename T, bool kFused>
+veda_status launch_few(const int8::MatArgs& p, const int8::QuantArgs& q, int sms, cudaStream_t s) {
+  if (p.M == 1) return launch_few_as<T, 1, kFused>(p, q, sms, s);
+  if (p.M == 2) return launch_few_as<T, 2, kFused>(p, q, sms, s);
+  if (p.M <= 4) return launch_few_as<T, 4, kFused>(p, q, sms, s);
+  return launch_few_as<T, 8, kFused>(p, q, sms, s);
+}
+// Small enough for the product to round its tokens itself.
+bool few_fused(int64_t M, int64_t kp) { return M <= int8::kFewMax && M * kp <= int8::kFewFused; }
 
 template <typename T>
 veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
@@ -1094,6 +1099,7 @@ veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w,
 size_t veda_int8_linear_workspace_bytes(int32_t M, int32_t K) {
   if (M <= 0 || K <= 0 || K > 131071) return 0;
   const size_t kp = (static_cast<size_t>(K) + 15) / 16 * 16;
+  if (few_fused(M, static_cast<int64_t>(kp))) return 0;
   return static_cast<size_t>(M) * kp + static_cast<size_t>(M) * sizeof(float);
 }
 
@@ -1105,15 +1111,12 @@ veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, c
       return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: bad size or type");
     if (K > 131071) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_linear: K above 131071 overflows the integer sum");
     if (M == 0 || N == 0) return VEDA_OK;
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < veda_int8_linear_workspace_bytes(M, K))
-      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: workspace too small or misaligned");
-    const size_t kp = (static_cast<size_t>(K) + 15) / 16 * 16;
-    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + static_cast<size_t>(M) * kp);
-    veda_status st = check_int8_product("veda_int8_linear", workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N);
-    if (st != VEDA_OK) return st;
-    const int64_t es = type_size(x_dtype);
-    if (M <= int8::kFewMax && static_cast<int64_t>(M) * static_cast<int64_t>(kp) <= int8::kFewFused && x_dtype == y_dtype) {
+    const int64_t kp = (static_cast<int64_t>(K) + 15) / 16 * 16, es = type_size(x_dtype);
+    veda_status st;
+    if (few_fused(M, kp)) {
       if (!x || !aligned(x, es)) return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: missing or misaligned buffer");
+      if ((st = check_int8_product("veda_int8_linear", w, w_scale, w, w_scale, bias, y, y_stride, y_dtype, M, N)) != VEDA_OK)
+        return st;
       int sms;
       if ((st = current_device(sms)) != VEDA_OK) return st;
       int8::MatArgs p{};
@@ -1121,13 +1124,18 @@ veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, c
       p.sw = w_scale; p.bias = bias; p.out = y; p.ldo = y_stride;
       p.M = M; p.N = N; p.kp = static_cast<int32_t>(kp);
       int8::QuantArgs q{};
-      q.x = x; q.x_stride = x_stride; q.K = K; q.kp = p.kp;
+      q.x = x; q.x_stride = x_stride; q.K = K; q.kp = p.kp; q.dtype = x_dtype;
       q.vec = aligned(x, 16) && (M == 1 || x_stride * es % 16 == 0);
       const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
       if (y_dtype == VEDA_BF16) return launch_few<__nv_bfloat16, true>(p, q, sms, cs);
       if (y_dtype == VEDA_FP16) return launch_few<__half, true>(p, q, sms, cs);
       return launch_few<float, true>(p, q, sms, cs);
     }
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < veda_int8_linear_workspace_bytes(M, K))
+      return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: workspace too small or misaligned");
+    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + static_cast<size_t>(M) * kp);
+    st = check_int8_product("veda_int8_linear", workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N);
+    if (st != VEDA_OK) return st;
     if ((st = veda_quantize_int8(x, x_stride, x_dtype, workspace, scale, M, K, stream)) != VEDA_OK) return st;
     return veda_int8_matmul(workspace, scale, w, w_scale, bias, y, y_stride, y_dtype, M, N, K, stream);
   });

@@ -677,13 +677,13 @@ def _span(t: torch.Tensor) -> Tuple[int, int]:
     return t.data_ptr(), t.data_ptr() + t.element_size() * n
 
 
-def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """A buffer for work on `stream` (None: the current one): taken from that stream's memory,
-    and kept from reuse until what the current stream does with it later has run."""
+def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
+    """A buffer beside `like` for work on `stream` (None: the current one): taken from that stream's
+    memory, and kept from reuse until what the current stream does with it later has run."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream())
     return t
 
@@ -789,7 +789,7 @@ def rotary_table(positions: torch.Tensor, inv_freq: np.ndarray, axis: Optional[n
         raise ValueError("inv_freq / axis: expected equal shapes [P]")
     axes, rows = positions.shape
     if out is None:
-        out = _new((rows, len(inv), 2), torch.float32, positions.device, stream)
+        out = _new(positions, (rows, len(inv), 2), torch.float32, stream)
     _need(out, torch.float32, "out", shape=(rows, len(inv), 2))
     _check("veda_rotary_table", lib().veda_rotary_table(
         _ptr(positions), axes, rows, inv.ctypes.data, ax.ctypes.data, len(inv), float(amplitude), _ptr(out),
@@ -806,7 +806,7 @@ def rotary(x: torch.Tensor, table: RotaryTable, rows: Optional[torch.Tensor] = N
     B, N, H, D = x.shape
     table._check()
     if out is None:
-        out = _new((B, N, H, D), x.dtype, x.device, stream)
+        out = _new(x, (B, N, H, D), x.dtype, stream)
     else:
         _need_strided(out, "out", 4, x.dtype, x.shape, written=True)
         _separate(out, x, "x", True)
@@ -831,9 +831,9 @@ def rotary_permute_pool(x: torch.Tensor, table: RotaryTable, maps: DeviceMaps, o
     _need_maps(maps, H, maps.Npad)
     table._check()
     if out is None:
-        out = _new((B, H, maps.Npad, D), torch.bfloat16, x.device, stream)
+        out = _new(x, (B, H, maps.Npad, D), torch.bfloat16, stream)
     if pooled is None:
-        pooled = _new((B, H, maps.Npad // 128, 3, D), torch.float32, x.device, stream)
+        pooled = _new(x, (B, H, maps.Npad // 128, 3, D), torch.float32, stream)
     _need(out, torch.bfloat16, "out", shape=(B, H, maps.Npad, D))
     _need(pooled, torch.float32, "pooled", shape=(B, H, maps.Npad // 128, 3, D))
     _separate(out, x, "x", False)
@@ -854,7 +854,7 @@ def rotary_unpermute(x_t: torch.Tensor, table: RotaryTable, maps: DeviceMaps, N:
     _need_maps(maps, H, Npad)
     table._check()
     if out is None:
-        out = _new((B, N, H, D), torch.bfloat16, x_t.device, stream)
+        out = _new(x_t, (B, N, H, D), torch.bfloat16, stream)
     _need(out, torch.bfloat16, "out", shape=(B, N, H, D))
     _separate(out, x_t, "x_t", False)
     _check("veda_rotary_unpermute", lib().veda_rotary_unpermute(
@@ -933,7 +933,7 @@ def _norm_fwd(x, x3, residual, params, residual_scale, kind, eps, out_dtype, out
     if residual is not None:
         residual = _rows3(residual, "residual", out_dtype, x3.shape)
     if out is None:
-        out = _new(x.shape, out_dtype, x.device, stream)
+        out = _new(x, x.shape, out_dtype, stream)
         out3 = out if out.dim() == 3 else out.unsqueeze(0)
     else:
         out3 = _rows3(out, "out", out_dtype, x3.shape, written=True)
@@ -941,7 +941,7 @@ def _norm_fwd(x, x3, residual, params, residual_scale, kind, eps, out_dtype, out
         _separate(out3, residual, "the residual", True)
     stats = mean = rstd = None
     if want_stats:
-        stats = NormStats(_new((B, N), torch.float32, x.device, stream), _new((B, N), torch.float32, x.device, stream))
+        stats = NormStats(_new(x, (B, N), torch.float32, stream), _new(x, (B, N), torch.float32, stream))
         mean, rstd = stats.mean.data_ptr(), stats.rstd.data_ptr()
     _check("veda_norm_fwd", lib().veda_norm_fwd(
         _rows(x3), _rows(residual), _rows(out3), params, residual_scale, mean, rstd, B, N, C, _norm_kind(kind), eps,
@@ -993,7 +993,7 @@ def _norm_bwd(dy, x, x3, stats, params, has, residual_grad, residual_scale, kind
     elif k != 2:
         raise ValueError("stats: the forward's statistics are needed (want_stats=True)")
     if out is None:
-        out = _new(x.shape, x.dtype, x.device, stream)
+        out = _new(x, x.shape, x.dtype, stream)
         out3 = out if out.dim() == 3 else out.unsqueeze(0)
     else:
         out3 = _rows3(out, "out", x.dtype, x3.shape, written=True)
@@ -1002,14 +1002,14 @@ def _norm_bwd(dy, x, x3, stats, params, has, residual_grad, residual_scale, kind
     gain, shift, weight, bias = has
     # the gradients of the vectors are rows of one buffer: [B] gain, [B] shift, weight, bias
     rows = B * gain + B * shift + weight + bias
-    vec = _new((rows, C), torch.float32, x.device, stream)
+    vec = _new(x, (rows, C), torch.float32, stream)
     take, at = [], 0
     for want, n in ((gain, B), (shift, B), (weight, 1), (bias, 1)):
         take.append(vec[at:at + n] if want else None)
         at += n * want
     dgain, dshift, dweight, dbias = take
     nbytes = lib().veda_norm_bwd_workspace_bytes(B, N, C)
-    work = _new((max(nbytes, 16),), torch.uint8, x.device, stream)
+    work = _new(x, (max(nbytes, 16),), torch.uint8, stream)
     _check("veda_norm_bwd", lib().veda_norm_bwd(
         _rows(dy3), _rows(x3), mean, rstd, _rows(res3), _rows(out3), params, residual_scale, _ptr(dgain),
         _ptr(dshift), _ptr(dweight), _ptr(dbias), work.data_ptr(), work.numel(), B, N, C, k, _stream(stream)))
@@ -1099,8 +1099,8 @@ def quantize_int8(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) 
     _need_strided(m, "x", 2)
     rows, K = m.shape
     if out is None:
-        out = Int8Rows(_new((rows, -(-K // 16) * 16), torch.int8, x.device, stream),
-                       _new((rows,), torch.float32, x.device, stream), K)
+        out = Int8Rows(_new(x, (rows, -(-K // 16) * 16), torch.int8, stream),
+                       _new(x, (rows,), torch.float32, stream), K)
     else:
         if out.K != K or out.rows != rows:
             raise ValueError(f"out: expected {rows} rows of {K} codes")
@@ -1126,7 +1126,7 @@ def int8_matmul(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
     if out is None:
         if out_dtype not in _DTYPE:
             raise TypeError(f"out_dtype: expected bfloat16, float16 or float32, got {out_dtype}")
-        out = _new((M, N), out_dtype, a.codes.device, stream)
+        out = _new(a.codes, (M, N), out_dtype, stream)
     else:
         _need_strided(out, "out", 2, None, (M, N), written=True)
         for t, n in ((a.codes, "a.codes"), (w.codes, "w.codes"), (a.scale, "a.scale"), (w.scale, "w.scale"),
@@ -1154,11 +1154,12 @@ def int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] = Non
     dt = x.dtype if out_dtype is None else out_dtype
     if dt not in _DTYPE:
         raise TypeError(f"out_dtype: expected bfloat16, float16 or float32, got {dt}")
-    out = _new((*x.shape[:-1], N), dt, x.device, stream)
-    work = _new((max(16, lib().veda_int8_linear_workspace_bytes(M, K)),), torch.uint8, x.device, stream)
+    out = _new(x, (*x.shape[:-1], N), dt, stream)
+    nbytes = lib().veda_int8_linear_workspace_bytes(M, K)
+    work = _new(x, (nbytes,), torch.uint8, stream) if nbytes else None
     _check("veda_int8_linear", lib().veda_int8_linear(
         m.data_ptr(), m.stride(0), _DTYPE[m.dtype], w.codes.data_ptr(), w.scale.data_ptr(), _ptr(bias),
-        out.data_ptr(), N, _DTYPE[dt], work.data_ptr(), work.numel(), M, N, K, _stream(stream)))
+        out.data_ptr(), N, _DTYPE[dt], _ptr(work), nbytes, M, N, K, _stream(stream)))
     return out
 
 

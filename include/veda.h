@@ -664,7 +664,8 @@ VEDA_API veda_status veda_int8_matmul(const void* a, const float* a_scale, const
                                       const float* bias, void* y, int64_t y_stride, int32_t dtype, int32_t M,
                                       int32_t N, int32_t K, veda_stream_t stream);
 
-/* Workspace bytes of veda_int8_linear: the codes and scales of M rows. */
+/* Workspace bytes of veda_int8_linear: the codes and scales of M rows (0 for a few short rows, which
+ * the product rounds itself). */
 VEDA_API size_t veda_int8_linear_workspace_bytes(int32_t M, int32_t K);
 
 /*
@@ -673,6 +674,7 @@ VEDA_API size_t veda_int8_linear_workspace_bytes(int32_t M, int32_t K);
  *   x          [M][K] of x_dtype, rows x_stride elements apart
  *   y          [M][N] of y_dtype (device, out), rows y_stride elements apart
  *   workspace  device scratch of >= veda_int8_linear_workspace_bytes(...) bytes, 16-byte aligned
+ *              (NULL where that is 0)
  */
 VEDA_API veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, const void* w,
                                       const float* w_scale, const float* bias, void* y, int64_t y_stride,

@@ -162,6 +162,16 @@ def test_linear_shapes_streams_graph(V):
             q, s = R.quantize(x.reshape(-1, 200))
             ref, e = _product(q, s, w.codes[:, :200], w.scale, bias)
             assert R.worst(y.reshape(-1, 96), ref, e, torch.bfloat16) <= 1
+    # one call equals the two: rounded by the product itself (few short rows) or beforehand
+    for rows, K, dt, ydt in ((1, 5120, "bf16", "bf16"), (3, 4101, "fp16", "fp32"), (8, 2048, "fp32", "bf16"),
+                             (8, 2049, "bf16", "bf16"), (2, 9000, "bf16", "fp16"), (1, 7, "fp32", "fp32")):
+        x = _rand(rows, K + 1, seed=K, dtype=TYPES[dt])[:, K % 2:K % 2 + K]
+        wk = V.quantize_int8(_rand(70, K, seed=K + 1))
+        a = V.int8_linear(x, wk, out_dtype=TYPES[ydt])
+        assert torch.equal(a, V.int8_matmul(V.quantize_int8(x), wk, out_dtype=TYPES[ydt]))
+        x[0, K // 2] = float("nan")
+        y = V.int8_linear(x, wk, out_dtype=torch.float32)
+        assert torch.isnan(y[0]).all() and torch.isfinite(y[1:]).all()
     for rows in (1, 40):
         x = _rand(rows, 200, seed=4, dtype=torch.bfloat16)
         ref = V.int8_linear(x, w, bias)
