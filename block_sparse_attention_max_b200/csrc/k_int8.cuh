@@ -278,7 +278,7 @@ struct MatArgs {
   int32_t chunks;        // K chunks of 128 codes
   int32_t tiles_n;
   int64_t tiles;
-  int32_t out_vec;       // every even column of out can be written with its neighbour
+  int32_t out_vec;       // rows of out start on 16-byte boundaries
 };
 
 __device__ __forceinline__ float scaled(int32_t acc, float sa, float sw, float bias) {
@@ -308,7 +308,7 @@ __device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t 
 }
 
 // ------------------------------------------------------------------------------------
-// Few tokens (M <= kFewMax): the weights are read once and that is the whole cost, so a warp
+// Few tokens (M <= kFewMax, kFewMaxFused): the weights are read once and that is the whole cost, so a warp
 // takes one output channel's row at a time, 16 bytes a lane with several loads in flight, and forms
 // the products of all tokens with four-way integer dot products. The tokens' codes come from global
 // memory (through L1) or, kFused, are made here: every CTA rounds the few rows of x into its shared
@@ -316,12 +316,16 @@ __device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t 
 // 10 KB a CTA and saves the separate launch; M x K is bounded (kFewFused) so that it stays small
 // beside the weights.
 // ------------------------------------------------------------------------------------
-constexpr int kFewMax = 8;
+// Products of 5,120 x 5,120 (1,024 x 1,024): 2 tokens 7.7 us (3.2) here, 10.7 (4.3) on the tensor
+// cores (int8_tokens_kernel); 4 tokens 13.4 (3.8) and 10.7 (4.4). The fused form also saves the launch
+// that rounds x (4.4 us), so it takes up to 4.
+constexpr int kFewMax = 2, kFewMaxFused = 4;
+constexpr int kSomeMax = 128;
 constexpr int kFewThreads = 256;
 constexpr int kFewFused = 16384;      // M * kp of the fused form
 // CTAs an SM, by the registers of MT tokens; the grid is that many, so that a warp's next channel
 // follows its last and its loads never pause
-template <int MT> constexpr int few_ctas() { return MT <= 2 ? 5 : MT == 4 ? 4 : 3; }
+template <int MT> constexpr int few_ctas() { return MT <= 2 ? 5 : 4; }
 
 template <typename T, int MT, bool kFused>
 __global__ void __launch_bounds__(kFewThreads, few_ctas<MT>()) few_tokens_kernel(const __grid_constant__ MatArgs p,
@@ -425,10 +429,12 @@ __global__ void __launch_bounds__(kFewThreads, few_ctas<MT>()) few_tokens_kernel
 //            into a kStages-deep ring; the bytes of both CTAs are counted on the leader's barrier
 //   warp 5 (leader)     MMA issuer (one thread): four kind::i8 MMAs (M 256, N kBN, K 32) a chunk into
 //            one of two accumulators; its commits free the stage in both CTAs
-//   warps 0..3 (both)   epilogue of the CTA's 128 rows, 64 columns at a time: accumulators through
-//            shared memory, so that a lane holds two neighbouring columns (their scales and biases
-//            in registers) and every row of the output is written in contiguous pieces whatever its
-//            alignment; overlaps the next tile's main loop
+//   warps 0..3 (both)   epilogue of the CTA's 128 rows, 128 bytes of output a row at a time: a thread
+//            scales and rounds its own row (the channels' scales and biases as broadcasts from shared
+//            memory), stages it, and the warp writes the staged rows in contiguous pieces whatever
+//            their alignment; overlaps the next tile's main loop. (Scaling after the staging, a row at
+//            a time with a lane on two columns, is a chain of dependent steps: it took 20,000 cycles a
+//            tile, as long as the main loop over K = 5,120, and this a tenth of that.)
 // Tiles run channel-fastest, so the pairs of one wave share a few rows of A and all of W from L2.
 // Every wait is bounded; on a timeout a CTA raises its abort flag, its roles leave their loops, the
 // other CTA's waits run out in turn, in-flight copies and MMAs are drained, and both meet at the
@@ -440,9 +446,10 @@ constexpr uint32_t kStageTotal = 6 * 32768;                   // ring bytes a CT
 template <int BN> constexpr uint32_t stage_bytes() { return 16384u + static_cast<uint32_t>(BN) * 64u; }
 template <int BN> constexpr int stages() { return static_cast<int>(kStageTotal / stage_bytes<BN>()); }
 constexpr int kMaxStages = 9;
-constexpr uint32_t kEpiStride = 66;                           // words a staged row: pairs free of bank conflicts
-constexpr uint32_t kEpiWarpBytes = 32 * kEpiStride * 4;
-constexpr uint32_t kSmemBytes = kStageTotal + 4 * kEpiWarpBytes + 1024;
+constexpr uint32_t kEpiStride = 128 + 16;                     // bytes a staged row: 16-byte accesses free of conflicts
+constexpr uint32_t kEpiWarpBytes = 32 * kEpiStride;
+constexpr uint32_t kOffScales = kStageTotal + 4 * kEpiWarpBytes;    // [2][2][256]: channel scales and biases
+constexpr uint32_t kSmemBytes = kOffScales + 2 * 2 * 256 * 4 + 1024;
 constexpr uint32_t kTmemCols = 512;
 static_assert(stages<64>() <= kMaxStages && stages<128>() <= kMaxStages, "barriers for every stage");
 
@@ -525,35 +532,61 @@ struct Bars {
   int abort;
 };
 
-// 32 rows x 64 columns of accumulators, staged in shared memory, to the output: lane l holds columns
-// n0 + 2 l and n0 + 2 l + 1; `sa` is the scale of row m0 + lane.
+// 128 bytes a row (W = 128 / sizeof(T) columns from n0) of 32 rows from m0: accumulators at `taddr` to
+// the output. `w`, `b`: the W columns' scales and biases in shared memory; sa: this lane's row's scale.
 template <typename T>
-__device__ __forceinline__ void store_staged(const MatArgs& p, const uint32_t* staged, int32_t m0, int32_t n0, uint32_t lane,
-                                             float sa) {
+__device__ __forceinline__ void store_columns(const MatArgs& p, uint32_t taddr, uint8_t* staged, const float* w,
+                                              const float* b, int32_t m0, int32_t n0, uint32_t lane, float sa) {
   using V = rotary::Vec<T>;
-  const int32_t n = n0 + 2 * static_cast<int32_t>(lane);
-  const bool have0 = n < p.N, have1 = n + 1 < p.N;
-  const float w0 = have0 ? __ldg(p.sw + n) : 0.f, w1 = have1 ? __ldg(p.sw + n + 1) : 0.f;
-  const float b0 = p.bias && have0 ? __ldg(p.bias + n) : 0.f, b1 = p.bias && have1 ? __ldg(p.bias + n + 1) : 0.f;
-  const int32_t rows = min(32, p.M - m0);
-  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(m0) * p.ldo + n;
-#pragma unroll 4
-  for (int32_t r = 0; r < rows; ++r, out += p.ldo) {
-    const int2 acc = *reinterpret_cast<const int2*>(staged + r * kEpiStride + 2 * lane);
-    const float s = __shfl_sync(0xffffffffu, sa, r);
-    const float y0 = scaled(acc.x, s, w0, b0), y1 = scaled(acc.y, s, w1, b1);
-    if (p.out_vec) {                          // ldo and the address are even
-      if (have1) {
-        T v[2] = {V::to(y0), V::to(y1)};
-        if (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(v);
-        else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(v);
-        continue;
+  constexpr int W = 128 / static_cast<int>(sizeof(T));
+#pragma unroll
+  for (int h = 0; h < W; h += 32) {
+    uint32_t r[32];
+    tmem_ld32_sync(taddr + h, r);
+#pragma unroll
+    for (int j = 0; j < 32; j += V::E) {
+      float y[V::E];
+#pragma unroll
+      for (int i = 0; i < V::E; i += 4) {
+        const float4 cw = *reinterpret_cast<const float4*>(w + h + j + i), cb = *reinterpret_cast<const float4*>(b + h + j + i);
+        y[i] = scaled(static_cast<int32_t>(r[j + i]), sa, cw.x, cb.x);
+        y[i + 1] = scaled(static_cast<int32_t>(r[j + i + 1]), sa, cw.y, cb.y);
+        y[i + 2] = scaled(static_cast<int32_t>(r[j + i + 2]), sa, cw.z, cb.z);
+        y[i + 3] = scaled(static_cast<int32_t>(r[j + i + 3]), sa, cw.w, cb.w);
       }
-    } else if (have1) {
-      out[1] = V::to(y1);
+      *reinterpret_cast<uint4*>(staged + lane * kEpiStride + (h + j) * sizeof(T)) = V::put(y);
     }
-    if (have0) out[0] = V::to(y0);
   }
+  __syncwarp();
+  const int32_t rows = min(32, p.M - m0), cols = min(W, p.N - n0);
+  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(m0) * p.ldo + n0;
+  if (p.out_vec && cols == W) {              // 8 lanes a row, 4 rows an instruction
+    const int32_t c = static_cast<int32_t>(lane & 7);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t row = 4 * i + static_cast<int32_t>(lane >> 3);
+      const uint4 v = *reinterpret_cast<const uint4*>(staged + row * kEpiStride + c * 16);
+      if (row < rows) *reinterpret_cast<uint4*>(out + row * p.ldo + c * V::E) = v;
+    }
+  } else {
+#pragma unroll 1
+    for (int32_t row = 0; row < rows; row += 8) {          // eight rows out of shared memory, then to the output
+      T v[8][W / 32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < W / 32; ++h)
+          v[i][h] = reinterpret_cast<const T*>(staged + (row + i) * kEpiStride)[32 * h + static_cast<int32_t>(lane)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < W / 32; ++h) {
+          const int32_t c = 32 * h + static_cast<int32_t>(lane);
+          if (row + i < rows && c < cols) out[(row + i) * p.ldo + c] = v[i][h];
+        }
+    }
+  }
+  __syncwarp();
 }
 
 template <typename T, int BN>
@@ -595,7 +628,7 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (warp < 4) {
-    uint32_t* staged = reinterpret_cast<uint32_t*>(smem + kStageTotal + warp * kEpiWarpBytes);
+    uint8_t* staged = smem + kStageTotal + warp * kEpiWarpBytes;
     uint32_t it = 0;
     for (int64_t t = pair; t < p.tiles; t += pairs, ++it) {
       const int32_t m0 = static_cast<int32_t>(t / p.tiles_n) * kBM + static_cast<int32_t>(rank * 128 + warp * 32);
@@ -603,23 +636,23 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__
       const uint32_t ab = it & 1;
       const int32_t m = m0 + static_cast<int32_t>(lane);
       const float sa = m < p.M ? __ldg(p.sa + m) : 0.f;
-      if (!attn::warp_wait_abort(smem_u32(&bars.acc_full[ab]), (it >> 1) & 1, abort, 70)) break;
+      float* w = reinterpret_cast<float*>(smem + kOffScales) + ab * 512;
+      float* b = w + 256;
+      for (int32_t c = static_cast<int32_t>(tid); c < BN; c += 128) {
+        const bool have = n0 + c < p.N;
+        w[c] = have ? __ldg(p.sw + n0 + c) : 0.f;
+        b[c] = have && p.bias ? __ldg(p.bias + n0 + c) : 0.f;
+      }
+      // the epilogue's four warps; one barrier a tile: the buffers alternate
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const bool ok = attn::warp_wait_abort(smem_u32(&bars.acc_full[ab]), (it >> 1) & 1, abort, 70);
       tc_fence_after();
+      constexpr int W = 128 / static_cast<int>(sizeof(T));
       const uint32_t taddr = tmem + ((warp * 32) << 16) + ab * 256;
 #pragma unroll 1
-      for (int cc = 0; cc < BN; cc += 64) {
+      for (int cc = 0; cc < BN && ok; cc += W) {
         if (n0 + cc >= p.N || m0 >= p.M) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          tmem_ld32_sync(taddr + cc + 32 * h, r);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            *reinterpret_cast<uint2*>(staged + lane * kEpiStride + 32 * h + j) = make_uint2(r[j], r[j + 1]);
-        }
-        __syncwarp();
-        store_staged<T>(p, staged, m0, n0 + cc, lane, sa);
-        __syncwarp();
+        store_columns<T>(p, taddr + cc, staged, w + cc, b + cc, m0, n0 + cc, lane, sa);
       }
       tc_fence_before();
       __syncwarp();
@@ -684,6 +717,196 @@ int8_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__
   tc_fence_after();
   if (warp == 5) tmem_dealloc2(tmem, kTmemCols);
 }
+
+// ------------------------------------------------------------------------------------
+// Some tokens (kFewMax < M <= 128): still bound by reading the weights, so the weights are the M side
+// of the MMAs (128 channels a tile, BN >= M tokens as columns) and K is split over the CTAs of a
+// cluster, so that a small N still fills the SMs; two CTAs share an SM, and one's set-up and reduction
+// hide behind the other's loads. The integer partial sums meet through distributed shared memory:
+// CTA r adds up and writes tokens r, r + S, ... Any split gives the same bits.
+// ------------------------------------------------------------------------------------
+namespace tokens {
+constexpr int kThreads = 192;
+constexpr int kMaxSplit = 8;
+constexpr uint32_t kRing = 110592;                            // 108 KB: two CTAs an SM
+template <int BN> constexpr uint32_t stage_bytes() { return 16384u + static_cast<uint32_t>(BN) * 128u; }
+template <int BN> constexpr int stages() { return static_cast<int>(kRing / stage_bytes<BN>()); }
+constexpr int kMaxStages = 6;
+constexpr uint32_t kSmemBytes = kRing + 1024;
+static_assert(stages<16>() <= kMaxStages && 128u * 128u * 4u <= kRing, "barriers; partial sums fit the ring");
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void mma_ss_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ int4 ld_cluster(uint32_t cluster_addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// This CTA's tokens (rank, rank + split, ...; a warp every fourth of them): sums over the cluster, scaled
+// and written. A lane has four channels; U tokens' loads from up to S CTAs are in flight together, as a
+// load from another CTA's shared memory takes as long as one from L2.
+template <typename T, int U, int S>
+__device__ __forceinline__ void write_tokens(const MatArgs& p, uint32_t sb, int32_t n0, int32_t rank, int32_t split,
+                                             uint32_t warp, uint32_t lane) {
+  using V = rotary::Vec<T>;
+  const int32_t n = n0 + 4 * static_cast<int32_t>(lane), step = 4 * split;
+  float sw[4], bias[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sw[i] = n + i < p.N ? __ldg(p.sw + n + i) : 0.f;
+    bias[i] = n + i < p.N && p.bias ? __ldg(p.bias + n + i) : 0.f;
+  }
+  uint32_t peer[S];
+#pragma unroll
+  for (int i = 0; i < S; ++i) peer[i] = map_to_cta(sb + lane * 16u, static_cast<uint32_t>(i < split ? i : 0));
+  for (int32_t m0 = rank + static_cast<int32_t>(warp) * split; m0 < p.M; m0 += U * step) {
+    int4 part[U][S];
+    float sa[U];
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int32_t m = m0 + t * step;
+      sa[t] = m < p.M ? __ldg(p.sa + m) : 0.f;
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        part[t][i] = i < split && m < p.M ? ld_cluster(peer[i] + static_cast<uint32_t>(m) * 512u) : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int32_t m = m0 + t * step;
+      if (m >= p.M) continue;
+      int32_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        acc[0] += part[t][i].x;
+        acc[1] += part[t][i].y;
+        acc[2] += part[t][i].z;
+        acc[3] += part[t][i].w;
+      }
+      T y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = V::to(scaled(acc[i], sa[t], sw[i], bias[i]));
+      T* out = static_cast<T*>(p.out) + m * p.ldo + n;
+      if (p.out_vec && n + 4 <= p.N) {
+        if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+        else *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) out[i] = y[i];
+      }
+    }
+  }
+}
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(kThreads, 2)
+int8_tokens_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
+                   const __grid_constant__ MatArgs p, const int32_t split) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) Bars bars;
+  constexpr int kStages = stages<BN>();
+  constexpr uint32_t kStageB = stage_bytes<BN>();
+  constexpr uint32_t kCols = BN < 32 ? 32 : BN;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t rank = static_cast<int32_t>(cluster_rank());
+  const int32_t n0 = static_cast<int32_t>(blockIdx.x / split) * 128;
+  const int32_t c0 = static_cast<int32_t>(static_cast<int64_t>(p.chunks) * rank / split);
+  const int32_t c1 = static_cast<int32_t>(static_cast<int64_t>(p.chunks) * (rank + 1) / split);   // > c0: split <= chunks
+  volatile int* abort = &bars.abort;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 1);
+      mbar_init(smem_u32(&bars.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&bars.acc_full), 1);
+    mbar_init(smem_u32(&bars.drain), 1);
+    bars.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&bars.tmem_base), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+
+  if (warp == 4 && lane == 0) {
+    uint32_t g = 0;
+    for (int32_t c = c0; c < c1; ++c, ++g) {
+      const uint32_t s = g % kStages;
+      if (g >= kStages && !mbar_wait(smem_u32(&bars.empty[s]), (g / kStages - 1) & 1, abort, 80)) break;
+      mbar_arrive_expect_tx(smem_u32(&bars.full[s]), kStageB);
+      tma_load_2d(sb + s * kStageB, &mW, smem_u32(&bars.full[s]), c * 128, n0);
+      tma_load_2d(sb + s * kStageB + 16384u, &mX, smem_u32(&bars.full[s]), c * 128, 0);
+    }
+    for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i)
+      mbar_wait(smem_u32(&bars.full[i % kStages]), (i / kStages) & 1, nullptr, 81);
+  } else if (warp == 5 && lane == 0) {
+    constexpr uint32_t kIdesc = idesc_s8_s32(128, BN);
+    uint32_t g = 0;
+    for (int32_t c = c0; c < c1; ++c, ++g) {
+      const uint32_t s = g % kStages;
+      if (!mbar_wait(smem_u32(&bars.full[s]), (g / kStages) & 1, abort, 82)) break;
+      tc_fence_after();
+      const uint64_t dW = smem_desc_sw128(sb + s * kStageB, 16, 1024);
+      const uint64_t dX = smem_desc_sw128(sb + s * kStageB + 16384u, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) mma_ss_i8(tmem, dW + kk * 2, dX + kk * 2, kIdesc, (c > c0 || kk > 0) ? 1u : 0u);
+      tc_commit(smem_u32(&bars.empty[s]));
+    }
+    tc_commit(smem_u32(&bars.acc_full));
+    tc_commit(smem_u32(&bars.drain));
+    mbar_wait(smem_u32(&bars.drain), 0, nullptr, 83);
+  }
+  // partial sums [token][channel] over the ring, whose last stage the MMAs have read
+  int32_t* partial = reinterpret_cast<int32_t*>(smem);
+  if (warp < 4) {
+    if (attn::warp_wait_abort(smem_u32(&bars.acc_full), 0, abort, 84)) {
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((warp * 32) << 16);
+#pragma unroll
+      for (int cc = 0; cc < static_cast<int>(kCols); cc += 32) {
+        uint32_t r[32];
+        tmem_ld32_sync(taddr + cc, r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (cc + j < BN && cc + j < p.M) partial[(cc + j) * 128 + static_cast<int32_t>(warp * 32 + lane)] = static_cast<int32_t>(r[j]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();                                             // every CTA's partial sums are written
+  if (warp < 4) {
+    if (split <= 2) write_tokens<T, 8, 2>(p, sb, n0, rank, split, warp, lane);
+    else if (split <= 4) write_tokens<T, 4, 4>(p, sb, n0, rank, split, warp, lane);
+    else write_tokens<T, 2, 8>(p, sb, n0, rank, split, warp, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                             // no CTA's sums are read any more
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, kCols);
+}
+}  // namespace tokens
 
 }  // namespace int8
 }  // namespace veda

@@ -183,30 +183,40 @@ struct Own {
   __device__ __forceinline__ bool any(int j) const { return (vec ? first(j) : me + j * kVec * threads) < C; }
 };
 
-// This thread's share of a row of T into its own ring slots (slot stride: `threads` units).
+// This thread's share of a row of T on its way into its own ring slots (slot stride: `threads`
+// units). Aligned rows go there by asynchronous copies. Other rows have only plain loads: start()
+// issues them into registers, finish() -- a row's work later -- writes the ring.
 template <typename T, int NV, typename O>
-__device__ __forceinline__ void fetch_row(uint4* ring, const T* row, const O& o) {
-  constexpr int U = units_of<T>();
-  if (o.vec) {
+struct Fetch {
+  static constexpr int U = units_of<T>();
+  uint4 held[O::vec ? 1 : NV][O::vec ? 1 : U];
+  __device__ __forceinline__ void start(uint4* ring, const T* row, const O& o) {
+    if constexpr (O::vec) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (o.first(j) >= o.C) continue;
+      for (int j = 0; j < NV; ++j) {
+        if (o.first(j) >= o.C) continue;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        cp_async16(ring + (j * U + u) * o.threads, reinterpret_cast<const uint4*>(row + o.first(j)) + u);
-    }
-  } else {
+        for (int u = 0; u < U; ++u)
+          cp_async16(ring + (j * U + u) * o.threads, reinterpret_cast<const uint4*>(row + o.first(j)) + u);
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      uint4 tmp[U];
-      T* p = reinterpret_cast<T*>(tmp);
+      for (int j = 0; j < NV; ++j) {
+        T* p = reinterpret_cast<T*>(held[j]);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) p[i] = o.one(j, i) < o.C ? row[o.one(j, i)] : from_f<T>(0.f);
-#pragma unroll
-      for (int u = 0; u < U; ++u) ring[(j * U + u) * o.threads] = tmp[u];
+        for (int i = 0; i < kVec; ++i) p[i] = o.one(j, i) < o.C ? row[o.one(j, i)] : from_f<T>(0.f);
+      }
     }
   }
-}
+  __device__ __forceinline__ void finish(uint4* ring, const O& o) const {
+    if constexpr (!O::vec) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u) ring[(j * U + u) * o.threads] = held[j][u];
+    }
+  }
+};
 
 // Vector j of a ring row (zeros where the thread owns nothing).
 template <typename T, typename O>
@@ -349,20 +359,29 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
   y += first * a.yn;
   const int64_t xstep = step * a.xn, rstep = step * a.rn, ystep = step * a.yn;
   int32_t next = first;
-  auto fetch = [&](uint4* slot) {
+  Fetch<TI, NV, Own<kAligned>> fx;
+  Fetch<TO, NV, Own<kAligned>> fr;
+  auto start = [&](uint4* slot) {
     if (next < s.hi) {
-      fetch_row<TI, NV>(slot, x, o);
-      if (has_res) fetch_row<TO, NV>(slot + NV * UI * threads, res, o);
+      fx.start(slot, x, o);
+      if (has_res) fr.start(slot + NV * UI * threads, res, o);
     }
     cp_async_commit();
     x += xstep;
     res += rstep;
     next += step;
   };
+  auto finish = [&](uint4* slot) {           // of a row past the slice: stale values that no one reads
+    fx.finish(slot, o);
+    if (has_res) fr.finish(slot + NV * UI * threads, o);
+  };
   const int32_t stages = a.stages;
   uint4* const ring_end = ring + stages * stage_units;
   uint4* free_slot = ring;
-  for (int i = 0; i < stages - 1; ++i, free_slot += stage_units) fetch(free_slot);
+  for (int i = 0; i < stages - 1; ++i, free_slot += stage_units) {
+    start(free_slot);
+    finish(free_slot);
+  }
 
   // A and S of this thread's channels
   f2 A[NV][kPairs], S[NV][kPairs];
@@ -404,7 +423,7 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
     f2 v[NV][kPairs];
 #pragma unroll
     for (int j = 0; j < NV; ++j) read_vec<TI>(slot, j, o, v[j]);
-    fetch(free_slot);                              // the slot read in the previous round
+    start(free_slot);                              // the slot read in the previous round
     float mean = 0.f, rstd = 1.f;
     if (a.kind == kLayer) {
       f2 t = 0ull;
@@ -462,6 +481,7 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
       store_vec<TO>(y, j, o, v[j]);
     }
     y += ystep;
+    finish(free_slot);
     free_slot = slot;
     slot = slot + stage_units == ring_end ? ring : slot + stage_units;
   }
@@ -501,11 +521,13 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
   dx += first * a.yn;
   const int64_t xstep = step * a.xn, dstep = step * a.dn, rstep = step * a.rn, ystep = step * a.yn;
   int32_t next = first;
-  auto fetch = [&](uint4* slot) {
+  Fetch<TI, NV, Own<kAligned>> fx, fr;
+  Fetch<TO, NV, Own<kAligned>> fd;
+  auto start = [&](uint4* slot) {
     if (next < s.hi) {
-      fetch_row<TI, NV>(slot, x, o);
-      fetch_row<TO, NV>(slot + NV * UI * threads, dy, o);
-      if (has_res) fetch_row<TI, NV>(slot + NV * (UI + UO) * threads, res, o);
+      fx.start(slot, x, o);
+      fd.start(slot + NV * UI * threads, dy, o);
+      if (has_res) fr.start(slot + NV * (UI + UO) * threads, res, o);
     }
     cp_async_commit();
     x += xstep;
@@ -513,10 +535,18 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
     res += rstep;
     next += step;
   };
+  auto finish = [&](uint4* slot) {           // of a row past the slice: stale values that no one reads
+    fx.finish(slot, o);
+    fd.finish(slot + NV * UI * threads, o);
+    if (has_res) fr.finish(slot + NV * (UI + UO) * threads, o);
+  };
   const int32_t stages = a.stages;
   uint4* const ring_end = ring + stages * stage_units;
   uint4* free_slot = ring;
-  for (int i = 0; i < stages - 1; ++i, free_slot += stage_units) fetch(free_slot);
+  for (int i = 0; i < stages - 1; ++i, free_slot += stage_units) {
+    start(free_slot);
+    finish(free_slot);
+  }
 
   f2 A[NV][kPairs], P1[NV][kPairs], P2[NV][kPairs];
   {
@@ -570,7 +600,7 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
         t2 = fma2(q, xh[i], t2);
       }
     }
-    fetch(free_slot);                              // the slot read in the previous round
+    start(free_slot);                              // the slot read in the previous round
     float c1 = 0.f, c2 = 0.f;
     if (a.kind != kNone) {
       float sum[2] = {split(t1).x + split(t1).y, split(t2).x + split(t2).y};
@@ -597,6 +627,7 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
       store_vec<TI>(dx, j, o, g);
     }
     dx += ystep;
+    finish(free_slot);
     free_slot = slot;
     slot = slot + stage_units == ring_end ? ring : slot + stage_units;
   }

@@ -117,11 +117,16 @@ template <> struct Vec<float> {
 
 // ------------------------------------------------------------------------------------
 // Raster rotation. x, y: element strides (batch, token, head), channels contiguous; y may be x.
-// A head's row is cut into items: one item = VE pairs (kVec: one 16-byte vector of an
-// interleaved row, two vectors of a half-layout row; otherwise one pair), then the
-// pass-through channels in items of the same width. Lane c of a unit's warp takes item c (and
-// c + 32, ...) of every head, so its cos / sin stay in registers while it walks the heads;
-// rows of fewer than 32 items put 32 / width heads side by side in the warp.
+// A head's row is cut into items of vectors of W channels. kTwo: an item is two vectors whose channels
+// pair up one by one -- W channels of either half (half layout), or a channel and its neighbour
+// (interleaved rows without any vector); the channels behind the turned ones follow in items of two
+// vectors. Otherwise (interleaved) an item is one vector, W / 2 pairs, of which the last turned item may
+// hold some that are not. W is the widest that lengths, strides and addresses allow.
+//
+// A warp takes a token (a group of its heads). With many heads lane c takes item c (and c + 32, ...)
+// of every head, so its cos / sin stay in registers while it walks the heads, U at a time; rows of
+// fewer than 32 items put several heads side by side in the warp. kFlat: with few heads there is
+// nothing to keep, and a lane takes U items at a time of all of the token's.
 // ------------------------------------------------------------------------------------
 struct Args {
   const void* x;
@@ -134,16 +139,24 @@ struct Args {
   int64_t units;           // B * N * groups
   int32_t N, H, D, P;
   int32_t groups, hg;      // head groups per token, heads per group
-  int32_t width_log2;      // lanes per head row
+  int32_t width_log2;      // lanes per head row (not flat)
   int32_t items, rot_items;
+  int32_t apart;           // kTwo: channels between the two vectors of a turned item (P, or 1: interleaved)
   float sign;
 };
 
-template <typename T, bool kHalf, bool kVec>
+template <int BYTES> struct Word;
+template <> struct Word<16> { typedef uint4 type; };
+template <> struct Word<8> { typedef uint2 type; };
+template <> struct Word<4> { typedef uint32_t type; };
+template <> struct Word<2> { typedef uint16_t type; };
+
+template <typename T, bool kTwo, int W, bool kFlat>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Args a) {
   using V = Vec<T>;
-  constexpr int VE = kVec ? (kHalf ? V::E : V::E / 2) : 1;   // pairs per item
-  constexpr int U = 4;                                       // heads in flight per lane
+  using R = typename Word<W * static_cast<int>(sizeof(T))>::type;
+  constexpr int NP = kTwo ? W : W / 2;                       // pairs per item
+  constexpr int U = kFlat && W * sizeof(T) == 16 ? 2 : 4;    // items in flight per lane
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (unit >= a.units) return;
   const int32_t lane = threadIdx.x & 31;
@@ -160,108 +173,109 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   T* y = static_cast<T*>(a.y) + b * a.ys[0] + n * a.ys[1];
   const float2* cs = a.cs + row * a.P;
   const int32_t h0 = grp * a.hg, h1 = min(a.H, h0 + a.hg);
-  const int32_t width = 1 << a.width_log2, hstep = 32 >> a.width_log2;
-  for (int32_t c = lane & (width - 1); c < a.items; c += width) {
-    const bool turn = c < a.rot_items;
-    float co[VE], si[VE];
-    int32_t o1, o2;            // first channels of the item's two parts (kVec interleaved: one)
-    bool second = true;
-    if (turn) {
-      const int32_t p = c * VE;
-      o1 = kHalf ? p : 2 * p;
-      o2 = kHalf ? p + a.P : 2 * p + 1;
-      if constexpr (VE % 2 == 0) {
-        const float4* t = reinterpret_cast<const float4*>(cs + p);
+
+  struct Item {
+    int32_t o1, o2;          // first channels of its vectors
+    int32_t live;            // turned pairs (the first ones)
+    bool second;             // the second vector exists (kTwo)
+  };
+  const auto item_of = [&](int32_t c) {
+    Item t;
+    if (kTwo) {
+      const bool turn = c < a.rot_items;
+      t.o1 = turn ? (a.apart == 1 ? 2 * c : c * W) : 2 * a.P + (c - a.rot_items) * 2 * W;
+      t.o2 = t.o1 + (turn ? a.apart : W);
+      t.live = turn ? NP : 0;
+      t.second = t.o2 < a.D;
+    } else {
+      t.o1 = t.o2 = c * W;
+      t.live = min(NP, max(0, a.P - c * NP));
+      t.second = false;
+    }
+    return t;
+  };
+  struct Turns { float c[NP], s[NP]; };
+  const auto load_turns = [&](int32_t c, int32_t live, Turns& t) {
+    const float2* p = cs + c * NP;
+    if (NP % 2 == 0 && live == NP && a.P % 2 == 0) {          // 16-byte aligned
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) {
-          const float4 v = __ldg(t + i);
-          co[2 * i] = v.x; si[2 * i] = v.y * a.sign;
-          co[2 * i + 1] = v.z; si[2 * i + 1] = v.w * a.sign;
-        }
-      } else {
-        const float2 v = __ldg(cs + p);
-        co[0] = v.x; si[0] = v.y * a.sign;
+      for (int i = 0; i + 1 < NP; i += 2) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+        t.c[i] = v.x; t.s[i] = v.y * a.sign;
+        t.c[i + 1] = v.z; t.s[i + 1] = v.w * a.sign;
       }
     } else {
-      constexpr int W = kVec ? (kHalf ? 2 * V::E : V::E) : 2;   // channels per item
-      o1 = 2 * a.P + (c - a.rot_items) * W;
-      o2 = o1 + (kVec ? V::E : 1);
-      second = o2 < a.D;
 #pragma unroll
-      for (int i = 0; i < VE; ++i) { co[i] = 1.f; si[i] = 0.f; }
+      for (int i = 0; i < NP; ++i) {
+        const float2 v = i < live ? __ldg(p + i) : make_float2(1.f, 0.f);
+        t.c[i] = v.x; t.s[i] = v.y * a.sign;
+      }
     }
-    if (bad) {                  // a flagged token's channels are written as zeros
+  };
+  const auto load = [&](const Item& t, int32_t h, R& v1, R& v2) {
+    const T* r = x + h * a.xs[2];
+    v1 = *reinterpret_cast<const R*>(r + t.o1);
+    if (kTwo && t.second) v2 = *reinterpret_cast<const R*>(r + t.o2);
+  };
+  // turns the pairs that are to be turned (the others' bits stay as they are) and stores
+  const auto finish = [&](const Item& t, const Turns& w, int32_t h, R v1, R v2) {
+    T* r = y + h * a.ys[2];
+    if (bad) v1 = v2 = R{};                                   // a flagged token is written as zeros
+    T* e1 = reinterpret_cast<T*>(&v1);
+    T* e2 = reinterpret_cast<T*>(&v2);
+    if (t.live > 0 && !bad) {
 #pragma unroll
-      for (int i = 0; i < VE; ++i) co[i] = si[i] = 0.f;
+      for (int i = 0; i < NP; ++i) {
+        T& first = kTwo ? e1[i] : e1[2 * i];
+        T& second = kTwo ? e2[i] : e1[2 * i + 1];
+        const float f = V::one(first), g = V::one(second);
+        const T nf = V::to(fmaf(f, w.c[i], -(g * w.s[i]))), ng = V::to(fmaf(g, w.c[i], f * w.s[i]));
+        if (kTwo || i < t.live) {
+          first = nf;
+          second = ng;
+        }
+      }
     }
-    for (int32_t h = h0 + (lane >> a.width_log2); h < h1; h += U * hstep) {
-      if constexpr (kVec) {
-        uint4 v1[U], v2[U];
+    *reinterpret_cast<R*>(r + t.o1) = v1;
+    if (kTwo && t.second) *reinterpret_cast<R*>(r + t.o2) = v2;
+  };
+
+  if (kFlat) {
+    const int32_t total = (h1 - h0) * a.items;
+    for (int32_t q = lane; q < total; q += 32 * U) {
+      Item t[U];
+      Turns w[U];
+      R v1[U], v2[U];
+      int32_t h[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int32_t hh = h + u * hstep;
-          if (hh >= h1) continue;
-          const T* r = x + hh * a.xs[2];
-          v1[u] = *reinterpret_cast<const uint4*>(r + o1);
-          if (kHalf && second) v2[u] = *reinterpret_cast<const uint4*>(r + o2);
-        }
+      for (int u = 0; u < U; ++u) {
+        const int32_t i = q + 32 * u;
+        if (i >= total) continue;
+        h[u] = i / a.items;
+        const int32_t c = i - h[u] * a.items;
+        h[u] += h0;
+        t[u] = item_of(c);
+        load(t[u], h[u], v1[u], v2[u]);
+        if (t[u].live > 0) load_turns(c, t[u].live, w[u]);
+      }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int32_t hh = h + u * hstep;
-          if (hh >= h1) continue;
-          T* r = y + hh * a.ys[2];
-          if (!turn) {          // pass-through: the bits as they are (zeros where flagged)
-            if (bad) v1[u] = v2[u] = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(r + o1) = v1[u];
-            if (kHalf && second) *reinterpret_cast<uint4*>(r + o2) = v2[u];
-            continue;
-          }
-          float f[V::E];
-          V::get(v1[u], f);
-          if constexpr (kHalf) {
-            float g[V::E];
-            V::get(v2[u], g);
-            float p[V::E], q[V::E];
+      for (int u = 0; u < U; ++u)
+        if (q + 32 * u < total) finish(t[u], w[u], h[u], v1[u], v2[u]);
+    }
+  } else {
+    const int32_t width = 1 << a.width_log2, hstep = 32 >> a.width_log2;
+    for (int32_t c = lane & (width - 1); c < a.items; c += width) {
+      const Item t = item_of(c);
+      Turns w;
+      if (t.live > 0) load_turns(c, t.live, w);
+      for (int32_t h = h0 + (lane >> a.width_log2); h < h1; h += U * hstep) {
+        R v1[U], v2[U];
 #pragma unroll
-            for (int i = 0; i < V::E; ++i) {
-              p[i] = bad ? 0.f : fmaf(f[i], co[i], -(g[i] * si[i]));
-              q[i] = bad ? 0.f : fmaf(g[i], co[i], f[i] * si[i]);
-            }
-            *reinterpret_cast<uint4*>(r + o1) = V::put(p);
-            *reinterpret_cast<uint4*>(r + o2) = V::put(q);
-          } else {
-            float p[V::E];
+        for (int u = 0; u < U; ++u)
+          if (h + u * hstep < h1) load(t, h + u * hstep, v1[u], v2[u]);
 #pragma unroll
-            for (int i = 0; i < V::E / 2; ++i) {
-              p[2 * i] = bad ? 0.f : fmaf(f[2 * i], co[i], -(f[2 * i + 1] * si[i]));
-              p[2 * i + 1] = bad ? 0.f : fmaf(f[2 * i + 1], co[i], f[2 * i] * si[i]);
-            }
-            *reinterpret_cast<uint4*>(r + o1) = V::put(p);
-          }
-        }
-      } else {
-        T t1[U], t2[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int32_t hh = h + u * hstep;
-          if (hh >= h1) continue;
-          t1[u] = x[hh * a.xs[2] + o1];
-          if (second) t2[u] = x[hh * a.xs[2] + o2];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int32_t hh = h + u * hstep;
-          if (hh >= h1) continue;
-          T* r = y + hh * a.ys[2];
-          if (!turn) {
-            r[o1] = bad ? V::to(0.f) : t1[u];
-            if (second) r[o2] = bad ? V::to(0.f) : t2[u];
-            continue;
-          }
-          const float f = V::one(t1[u]), g = V::one(t2[u]);
-          r[o1] = V::to(bad ? 0.f : fmaf(f, co[0], -(g * si[0])));
-          r[o2] = V::to(bad ? 0.f : fmaf(g, co[0], f * si[0]));
-        }
+        for (int u = 0; u < U; ++u)
+          if (h + u * hstep < h1) finish(t, w, h + u * hstep, v1[u], v2[u]);
       }
     }
   }

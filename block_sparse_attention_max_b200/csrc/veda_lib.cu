@@ -105,6 +105,18 @@ veda_status current_device(int& sms) {
         {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float, 64>), static_cast<int>(int8::kSmemBytes)},
         {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float, 128>), static_cast<int>(int8::kSmemBytes)},
         {reinterpret_cast<const void*>(int8::int8_gemm_kernel<float, 256>), static_cast<int>(int8::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__nv_bfloat16, 16>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__nv_bfloat16, 32>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__nv_bfloat16, 64>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__nv_bfloat16, 128>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__half, 16>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__half, 32>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__half, 64>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<__half, 128>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<float, 16>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<float, 32>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<float, 64>), static_cast<int>(int8::tokens::kSmemBytes)},
+        {reinterpret_cast<const void*>(int8::tokens::int8_tokens_kernel<float, 128>), static_cast<int>(int8::tokens::kSmemBytes)},
     };
     for (auto& x : attrs) {
       e = cudaFuncSetAttribute(x.f, cudaFuncAttributeMaxDynamicSharedMemorySize, x.bytes);
@@ -282,6 +294,25 @@ veda_status check_int8_product(const char* call, const void* a, const float* a_s
   return VEDA_OK;
 }
 
+template <typename T, bool kTwo, int W>
+void launch_rotary_as(const rotary::Args& a, bool flat, unsigned blocks, cudaStream_t s) {
+  if (flat) rotary::rotary_kernel<T, kTwo, W, true><<<blocks, rotary::kThreads, 0, s>>>(a);
+  else rotary::rotary_kernel<T, kTwo, W, false><<<blocks, rotary::kThreads, 0, s>>>(a);
+}
+template <typename T>
+void launch_rotary(const rotary::Args& a, bool two, int32_t W, bool flat, unsigned blocks, cudaStream_t s) {
+  constexpr int E = static_cast<int>(16 / sizeof(T));
+  if (two) {
+    if (W == E) return launch_rotary_as<T, true, E>(a, flat, blocks, s);
+    if (W == E / 2) return launch_rotary_as<T, true, E / 2>(a, flat, blocks, s);
+    if constexpr (sizeof(T) == 2)
+      if (W == 2) return launch_rotary_as<T, true, 2>(a, flat, blocks, s);
+    return launch_rotary_as<T, true, 1>(a, flat, blocks, s);
+  }
+  if (W == E) return launch_rotary_as<T, false, E>(a, flat, blocks, s);
+  launch_rotary_as<T, false, E / 2>(a, flat, blocks, s);
+}
+
 // Heads in groups of at most 8, as equal as they come; 24 warps an SM (80 registers a thread).
 veda_status launch_rotary_tiles(rotary::TileArgs& p, bool half_layout, bool gather, int sms, cudaStream_t s) {
   p.groups = (p.g.H + rotary::kTileHeads - 1) / rotary::kTileHeads;
@@ -328,15 +359,57 @@ template <typename T, bool kFused>
 veda_status launch_few(const int8::MatArgs& p, const int8::QuantArgs& q, int sms, cudaStream_t s) {
   if (p.M == 1) return launch_few_as<T, 1, kFused>(p, q, sms, s);
   if (p.M == 2) return launch_few_as<T, 2, kFused>(p, q, sms, s);
-  if (p.M <= 4) return launch_few_as<T, 4, kFused>(p, q, sms, s);
-  return launch_few_as<T, 8, kFused>(p, q, sms, s);
+  if constexpr (kFused) return launch_few_as<T, 4, true>(p, q, sms, s);
+  return fail(VEDA_ERR_UNSUPPORTED, "few_tokens_kernel: too many tokens");
 }
 // Small enough for the product to round its tokens itself.
-bool few_fused(int64_t M, int64_t kp) { return M <= int8::kFewMax && M * kp <= int8::kFewFused; }
+bool few_fused(int64_t M, int64_t kp) { return M <= int8::kFewMaxFused && M * kp <= int8::kFewFused; }
+
+// Some tokens: the split of K that ends first, from the weights' bytes at an SM's share of the HBM rate
+// (a chunk of 16 KB takes 0.37 us, twice that with two CTAs an SM) and 2.5 us a CTA beside its loads.
+template <typename T>
+veda_status launch_tokens(int8::MatArgs& p, int sms, cudaStream_t s) {
+  const int64_t tiles = (p.N - 1) / 128 + 1;
+  const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  int split = 1;
+  double best = 1e300;
+  for (int w = 1; w <= std::min(int8::tokens::kMaxSplit, p.chunks); ++w) {
+    const int64_t ctas = tiles * w, waves = (ctas + 2 * sms - 1) / (2 * sms);
+    const double chunk = ctas > sms ? 0.74 : 0.37;
+    const double cost = waves * ((p.chunks + w - 1) / w * chunk + 2.5);
+    if (cost < best) {
+      best = cost;
+      split = w;
+    }
+  }
+  veda_status st = get_encoder();
+  if (st != VEDA_OK) return st;
+  CUtensorMap mW, mX;
+  if ((st = encode_codes(mW, p.w, p.kp, p.N, 128)) != VEDA_OK || (st = encode_codes(mX, p.a, p.kp, p.M, bn)) != VEDA_OK) return st;
+  if (tiles * split > INT32_MAX) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_matmul: too many channels");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
+  cfg.blockDim = dim3(int8::tokens::kThreads);
+  cfg.dynamicSmemBytes = int8::tokens::kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(split);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  auto* k = bn == 16   ? int8::tokens::int8_tokens_kernel<T, 16>
+            : bn == 32 ? int8::tokens::int8_tokens_kernel<T, 32>
+            : bn == 64 ? int8::tokens::int8_tokens_kernel<T, 64>
+                       : int8::tokens::int8_tokens_kernel<T, 128>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, mW, mX, static_cast<const int8::MatArgs&>(p), static_cast<int32_t>(split));
+  return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "int8_tokens_kernel");
+}
 
 template <typename T>
 veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
   if (p.M <= int8::kFewMax) return launch_few<T, false>(p, int8::QuantArgs{}, sms, s);
+  if (p.M <= int8::kSomeMax) return launch_tokens<T>(p, sms, s);
   veda_status st = get_encoder();
   if (st != VEDA_OK) return st;
   // Channels per tile: the width that ends first. A chunk of 128 codes costs a pair the slower of its
@@ -952,26 +1025,38 @@ veda_status veda_rotary(const void* x, const int64_t* x_strides, void* y, const 
     rotary::Args a{};
     a.x = x; a.y = y;
     bool same = x == y;
-    // 16-byte vectors: every row of x and y starts on such a boundary and the layout's parts are
-    // whole vectors; otherwise a lane takes one pair
-    const int32_t P = rot_dim / 2, E = static_cast<int32_t>(16 / es);
-    bool vec = aligned(x, 16) && aligned(y, 16) && D % E == 0 && (interleaved ? rot_dim % E == 0 : P % E == 0);
     for (int i = 0; i < 3; ++i) {
       a.xs[i] = x_strides[i];
       a.ys[i] = y_strides[i];
-      vec = vec && x_strides[i] % E == 0 && y_strides[i] % E == 0;
       same = same && x_strides[i] == y_strides[i];
     }
+    // the widest vectors that lengths, strides and addresses allow: 16, 8 or (16-bit half layout) 4
+    // bytes, else single channels
+    const int32_t P = rot_dim / 2;
+    int32_t W = static_cast<int32_t>(16 / es);
+    const auto fits = [&](int32_t w) {
+      bool ok = aligned(x, w * es) && aligned(y, w * es) && D % w == 0 && (interleaved || P % w == 0);
+      for (int i = 0; i < 3; ++i) ok = ok && x_strides[i] % w == 0 && y_strides[i] % w == 0;
+      return ok;
+    };
+    const int32_t narrow = interleaved || es == 4 ? 8 : 4;
+    while (W > 1 && !fits(W)) W = W * es > narrow ? W / 2 : 1;
+    const bool two = !interleaved || W == 1;
     a.cs = reinterpret_cast<const float2*>(cos_sin);
     a.rows = rows; a.table_rows = table_rows;
     a.batch_rows = table_rows == N ? 0 : N;
     a.N = N; a.H = H; a.D = D; a.P = P;
     a.sign = inverse ? -1.f : 1.f;
-    const int32_t VE = vec ? (interleaved ? E / 2 : E) : 1;
-    const int32_t W = vec ? (interleaved ? E : 2 * E) : 2;
-    a.rot_items = P / VE;
-    // in place, the channels behind the rotated ones stay where they are
-    a.items = a.rot_items + (same && !rows ? 0 : (D - rot_dim + W - 1) / W);
+    a.apart = interleaved ? 1 : P;
+    // in place, the channels behind the turned ones stay where they are
+    const bool rest = !(same && !rows);
+    if (two) {
+      a.rot_items = P / W;
+      a.items = a.rot_items + (rest ? (D - rot_dim + 2 * W - 1) / (2 * W) : 0);
+    } else {
+      a.rot_items = (rot_dim + W - 1) / W;
+      a.items = rest ? D / W : a.rot_items;
+    }
     a.width_log2 = 0;
     while (a.width_log2 < 5 && (1 << a.width_log2) < a.items) ++a.width_log2;
     int sms;
@@ -988,17 +1073,11 @@ veda_status veda_rotary(const void* x, const int64_t* x_strides, void* y, const 
     a.units = tokens * a.groups;
     const int64_t blocks = (a.units + rotary::kWarps - 1) / rotary::kWarps;
     if (blocks > INT32_MAX) return fail(VEDA_ERR_UNSUPPORTED, "veda_rotary: too many tokens");
-    using BF = __nv_bfloat16;
-    typedef void (*Kernel)(const rotary::Args);
-    static const Kernel kernels[3][2][2] = {   // [type][half layout][vectors]
-        {{rotary::rotary_kernel<BF, false, false>, rotary::rotary_kernel<BF, false, true>},
-         {rotary::rotary_kernel<BF, true, false>, rotary::rotary_kernel<BF, true, true>}},
-        {{rotary::rotary_kernel<__half, false, false>, rotary::rotary_kernel<__half, false, true>},
-         {rotary::rotary_kernel<__half, true, false>, rotary::rotary_kernel<__half, true, true>}},
-        {{rotary::rotary_kernel<float, false, false>, rotary::rotary_kernel<float, false, true>},
-         {rotary::rotary_kernel<float, true, false>, rotary::rotary_kernel<float, true, true>}}};
-    kernels[dtype][interleaved ? 0 : 1][vec ? 1 : 0]<<<static_cast<unsigned>(blocks), rotary::kThreads, 0,
-                                                       reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    const bool flat = a.hg <= 2 * side;                      // not two passes of four heads: nothing to keep
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == VEDA_BF16) launch_rotary<__nv_bfloat16>(a, two, W, flat, static_cast<unsigned>(blocks), s);
+    else if (dtype == VEDA_FP16) launch_rotary<__half>(a, two, W, flat, static_cast<unsigned>(blocks), s);
+    else launch_rotary<float>(a, two, W, flat, static_cast<unsigned>(blocks), s);
     return launched("rotary_kernel");
   });
 }
@@ -1088,7 +1167,7 @@ veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w,
     p.out = y; p.ldo = y_stride;
     p.M = M; p.N = N; p.kp = (K + 15) / 16 * 16;
     p.chunks = (p.kp + 127) / 128;
-    p.out_vec = aligned(y, 2 * es) && y_stride % 2 == 0;
+    p.out_vec = aligned(y, 16) && y_stride * es % 16 == 0;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == VEDA_BF16) return launch_int8<__nv_bfloat16>(p, sms, s);
     if (dtype == VEDA_FP16) return launch_int8<__half>(p, sms, s);

@@ -65,43 +65,51 @@ Shape shape_of(int32_t C, bool is_aligned, bool bwd, bool res) {
 
 typedef void (*Kernel)(const Args);
 
-// The kernels of one shape and type pair; null for a pair that is not built.
-template <int NV, bool W, int BOUND, bool A>
-Kernel pick_types(bool bwd, int32_t ti, int32_t to) {
+// The kernels of one shape for every type pair; null for a pair that is not built.
+template <template <typename, typename> class K>
+Kernel by_types(int32_t ti, int32_t to) {
   using B = __nv_bfloat16;
   using H = __half;
-#define VEDA_PAIR(TI, TO) (bwd ? norm::norm_bwd_kernel<TI, TO, (W ? NV : NV < 2 ? 1 : 2), W, BOUND, A> : norm::norm_fwd_kernel<TI, TO, NV, W, A>)
-  if (ti == VEDA_BF16 && to == VEDA_BF16) return VEDA_PAIR(B, B);
-  if (ti == VEDA_FP16 && to == VEDA_FP16) return VEDA_PAIR(H, H);
-  if (ti == VEDA_FP32 && to == VEDA_FP32) return VEDA_PAIR(float, float);
-  if (ti == VEDA_FP32 && to == VEDA_BF16) return VEDA_PAIR(float, B);
-  if (ti == VEDA_BF16 && to == VEDA_FP32) return VEDA_PAIR(B, float);
-#undef VEDA_PAIR
+  if (ti == VEDA_BF16 && to == VEDA_BF16) return K<B, B>::kernel();
+  if (ti == VEDA_FP16 && to == VEDA_FP16) return K<H, H>::kernel();
+  if (ti == VEDA_FP32 && to == VEDA_FP32) return K<float, float>::kernel();
+  if (ti == VEDA_FP32 && to == VEDA_BF16) return K<float, B>::kernel();
+  if (ti == VEDA_BF16 && to == VEDA_FP32) return K<B, float>::kernel();
   return nullptr;
 }
-template <bool A>
-Kernel pick_shape(const Shape& s, bool bwd, int32_t ti, int32_t to) {
-  if (s.warp) {
-    if (s.nv == 1) return pick_types<1, true, 256, A>(bwd, ti, to);
-    if (s.nv == 2) return pick_types<2, true, 256, A>(bwd, ti, to);
-    return pick_types<4, true, 256, A>(bwd, ti, to);
-  }
-  if (s.nv == 1) return pick_types<1, false, norm::kMaxThreads, A>(bwd, ti, to);
-  if (s.nv == 4) return pick_types<4, false, 320, A>(bwd, ti, to);          // forward only
-  return s.threads <= 320 ? pick_types<2, false, 320, A>(bwd, ti, to)
-                          : pick_types<2, false, norm::kMaxThreads, A>(bwd, ti, to);
-}
-// aligned: every row starts on a 16-byte boundary and C % 8 == 0
+template <int NV, bool W, bool A>
+struct Fwd {
+  template <typename TI, typename TO> struct K { static Kernel kernel() { return norm::norm_fwd_kernel<TI, TO, NV, W, A>; } };
+};
+template <int NV, bool W, int BOUND, bool A>
+struct Bwd {
+  template <typename TI, typename TO> struct K { static Kernel kernel() { return norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, A>; } };
+};
+constexpr int kMid = 320, kBig = norm::kMaxThreads;      // thread bounds of the CTA-per-row backward
+
+// is_aligned: every row starts on a 16-byte boundary and C % 8 == 0
 Kernel pick(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to) {
-  return is_aligned ? pick_shape<true>(s, bwd, ti, to) : pick_shape<false>(s, bwd, ti, to);
+  if (!is_aligned) {
+    if (s.warp) return bwd ? by_types<Bwd<1, true, 256, false>::K>(ti, to) : by_types<Fwd<1, true, false>::K>(ti, to);
+    if (s.nv == 1) return bwd ? by_types<Bwd<1, false, kBig, false>::K>(ti, to) : by_types<Fwd<1, false, false>::K>(ti, to);
+    if (!bwd) return by_types<Fwd<2, false, false>::K>(ti, to);
+    return s.threads <= kMid ? by_types<Bwd<2, false, kMid, false>::K>(ti, to) : by_types<Bwd<2, false, kBig, false>::K>(ti, to);
+  }
+  if (s.warp) {
+    if (s.nv == 1) return bwd ? by_types<Bwd<1, true, 256, true>::K>(ti, to) : by_types<Fwd<1, true, true>::K>(ti, to);
+    if (s.nv == 2) return bwd ? by_types<Bwd<2, true, 256, true>::K>(ti, to) : by_types<Fwd<2, true, true>::K>(ti, to);
+    return bwd ? by_types<Bwd<4, true, 256, true>::K>(ti, to) : by_types<Fwd<4, true, true>::K>(ti, to);
+  }
+  if (!bwd) return s.nv == 4 ? by_types<Fwd<4, false, true>::K>(ti, to) : by_types<Fwd<2, false, true>::K>(ti, to);
+  return s.threads <= kMid ? by_types<Bwd<2, false, kMid, true>::K>(ti, to) : by_types<Bwd<2, false, kBig, true>::K>(ti, to);
 }
 
 // Ring bytes of a CTA: every row a group has in flight, 16-byte units.
-int ring_bytes(const Shape& s, bool bwd, int32_t ti, int32_t to, bool res, int32_t& stages) {
+int ring_bytes(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to, bool res, int32_t& stages) {
   const int ui = ti == VEDA_FP32 ? 2 : 1, uo = to == VEDA_FP32 ? 2 : 1;
   const int units = bwd ? ui + uo + (res ? ui : 0) : ui + (res ? uo : 0);
   const int row = s.nv * units * s.threads * 16;            // <= 96 KB (fp32, 8,192 channels)
-  stages = bwd ? kBwdStages : kFwdStages;
+  stages = !is_aligned ? 2 : bwd ? kBwdStages : kFwdStages;   // plain loads: one row ahead
   while (stages > 2 && stages * row > kMaxRing) --stages;
   return stages * row;
 }
@@ -211,7 +219,7 @@ veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const v
     const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.y, a.yb, a.yn, y->dtype) &&
             (!residual || vec_rows(a.res, a.rb, a.rn, y->dtype));
     const Shape s = shape_of(C, vec, false, residual != nullptr);
-    const int bytes = ring_bytes(s, false, x->dtype, y->dtype, residual != nullptr, a.stages);
+    const int bytes = ring_bytes(s, false, vec, x->dtype, y->dtype, residual != nullptr, a.stages);
     const Kernel k = pick(s, false, vec, x->dtype, y->dtype);
     if ((st = slices_for(k, s, bytes, sms, kMaxPerSmFwd, B, N, a.slices)) != VEDA_OK) return st;
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a);
@@ -277,7 +285,7 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.dy, a.db, a.dn, dy->dtype) &&
             vec_rows(a.y, a.yb, a.yn, x->dtype) && (!a.res || vec_rows(a.res, a.rb, a.rn, x->dtype));
     const Shape s = shape_of(C, vec, true, a.res != nullptr);
-    const int bytes = ring_bytes(s, true, x->dtype, dy->dtype, a.res != nullptr, a.stages);
+    const int bytes = ring_bytes(s, true, vec, x->dtype, dy->dtype, a.res != nullptr, a.stages);
     a.part = static_cast<float*>(workspace);
     const Kernel k = pick(s, true, vec, x->dtype, dy->dtype);
     if ((st = slices_for(k, s, bytes, sms, kMaxPerSmBwd, B, N, a.slices)) != VEDA_OK) return st;

@@ -127,12 +127,12 @@ def test_int8_refusals(L):
 
     need = L.veda_int8_linear_workspace_bytes(9, 60)
     assert need >= 9 * 64 + 9 * 4 and L.veda_int8_linear_workspace_bytes(0, 60) == 0
-    assert L.veda_int8_linear_workspace_bytes(8, 2048) == 0 < L.veda_int8_linear_workspace_bytes(8, 2049)
+    assert L.veda_int8_linear_workspace_bytes(4, 4096) == 0 < L.veda_int8_linear_workspace_bytes(4, 4097)
 
     def lin(x=256, st=64, xdt=0, w=16, sw=16, bias=None, y=16, ys=32, dt=0, ws=16, nws=need, M=9, N=32, K=60):
         return L.veda_int8_linear(x, st, xdt, w, sw, bias, y, ys, dt, ws, nws, M, N, K, None)
     for bad in (dict(x=None), dict(w=None), dict(sw=None), dict(y=None), dict(x=255), dict(w=8), dict(xdt=3),
-                dict(dt=-1), dict(M=-1), dict(K=0), dict(ys=31), dict(bias=2)):
+                dict(dt=-1), dict(M=-1), dict(K=0), dict(ys=31), dict(bias=2)):   # with a workspace, and without
         assert lin(**bad) == INVALID and lin(**{**dict(M=4, ws=None, nws=0), **bad}) == INVALID, bad
     for bad in (dict(ws=None), dict(ws=8), dict(nws=need - 1)):
         assert lin(**bad) == INVALID, bad

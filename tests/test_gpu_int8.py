@@ -98,7 +98,8 @@ def _product(a, sa, w, sw, bias):
     return y, e
 
 
-SIZES = [(1, 1, 1), (1, 5, 17), (1, 257, 5120), (2, 100, 333), (3, 64, 48), (5, 1000, 640), (8, 130, 4101), (9, 1, 1),
+SIZES = [(1, 1, 1), (1, 5, 17), (1, 257, 5120), (2, 100, 333), (2, 3000, 64), (3, 127, 16), (4, 129, 5000), (7, 5200, 130),
+         (17, 600, 1100), (33, 128, 2000), (65, 1000, 700), (100, 70, 4097), (128, 2049, 384), (3, 64, 48), (5, 1000, 640), (8, 130, 4101), (9, 1, 1),
          (9, 33, 50), (16, 256, 128), (31, 300, 127), (64, 511, 1040), (127, 255, 129), (128, 256, 512), (129, 257, 513),
          (200, 640, 256), (300, 1030, 2064), (777, 515, 4101), (1000, 2600, 100), (2049, 96, 130)]
 
@@ -163,8 +164,9 @@ def test_linear_shapes_streams_graph(V):
             ref, e = _product(q, s, w.codes[:, :200], w.scale, bias)
             assert R.worst(y.reshape(-1, 96), ref, e, torch.bfloat16) <= 1
     # one call equals the two: rounded by the product itself (few short rows) or beforehand
-    for rows, K, dt, ydt in ((1, 5120, "bf16", "bf16"), (3, 4101, "fp16", "fp32"), (8, 2048, "fp32", "bf16"),
-                             (8, 2049, "bf16", "bf16"), (2, 9000, "bf16", "fp16"), (1, 7, "fp32", "fp32")):
+    for rows, K, dt, ydt in ((1, 5120, "bf16", "bf16"), (3, 4101, "fp16", "fp32"), (4, 4096, "fp32", "bf16"),
+                             (4, 4097, "bf16", "bf16"), (2, 9000, "bf16", "fp16"), (1, 7, "fp32", "fp32"),
+                             (5, 100, "bf16", "bf16")):
         x = _rand(rows, K + 1, seed=K, dtype=TYPES[dt])[:, K % 2:K % 2 + K]
         wk = V.quantize_int8(_rand(70, K, seed=K + 1))
         a = V.int8_linear(x, wk, out_dtype=TYPES[ydt])

@@ -56,7 +56,8 @@ def test_table(V, rows, dims, amp):
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("B,N,H,D,rot", [(1, 1, 1, 2, 2), (1, 1, 40, 128, 128), (2, 37, 8, 128, 64), (3, 5, 1, 96, 30),
                                          (2, 130, 3, 80, 80), (1, 300, 17, 256, 256), (1, 3, 2, 640, 512),
-                                         (2, 9, 5, 33, 18), (1, 1025, 12, 64, 48)])
+                                         (2, 9, 5, 33, 18), (1, 1025, 12, 64, 48), (1, 1300, 1, 256, 86),
+                                         (1, 1300, 40, 64, 20), (2, 700, 33, 72, 24), (1, 2000, 17, 36, 14), (3, 50, 2, 128, 2)])
 def test_rotary_matches_definition(V, dtype, layout, B, N, H, D, rot):
     dt, inter = TYPES[dtype], layout == "interleaved"
     x = _rand(B, N, H, D, seed=D + rot, dtype=dt)
@@ -129,6 +130,17 @@ def test_empty_and_nonfinite(V):
     ok = torch.ones_like(y, dtype=torch.bool)
     ok[0, 1, 0, 4:6] = ok[0, 2, 1, 8:10] = False                                # their pairs only
     assert torch.isfinite(y[ok]).all() and not torch.isfinite(y[~ok]).any()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_channels_behind_the_turned_ones_keep_their_bits(V, layout):
+    """A vector may hold turned and other channels: NaN, infinities and signs of the others stay."""
+    x = _rand(2, 40, 3, 64, seed=20, dtype=torch.bfloat16)
+    x[..., 22:26] = torch.tensor([float("nan"), float("-inf"), -0.0, float("inf")], device=DEV)
+    t = _table(V, 40, 22, layout == "interleaved")
+    for y in (V.rotary(x, t), V.rotary(x.clone(), t, out=None)):
+        assert torch.equal(y[..., 22:].view(torch.int16), x[..., 22:].view(torch.int16))
+        assert torch.isfinite(y[..., :22]).all()
 
 
 def test_gradient_is_the_transpose(V):
