@@ -90,6 +90,9 @@ __device__ __forceinline__ uint32_t shared_addr(const void* p) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_addr(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(shared_addr(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -168,19 +171,29 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return v > 0x1p-120f && v < 0x1p120f ? n : r;     // the step itself would leave fp32's range
 }
 
-// Which channels thread `me` of `threads` owns. Aligned rows: whole vectors, j of them `threads`
-// vectors apart. Other rows have no 16-byte accesses, so there a thread's channels lie `threads`
-// apart and every access of a warp is one contiguous piece.
-template <bool kAligned>
+// Which channels thread `me` of `threads` owns: NV vectors of two halves of four channels.
+//   kVectors: a vector is eight neighbouring channels, vectors `threads` apart (16-byte accesses of
+//     16-bit types);
+//   kHalves: every half is on its own, halves `threads` apart, so that the accesses of a warp to fp32
+//     rows are contiguous too (two 16-byte accesses a vector 32 bytes apart fetch every sector twice:
+//     58% of the HBM copy rate where this has 80%); 16-bit rows beside them move in 8-byte pieces;
+//   kSingle: rows without 16-byte boundaries: every channel on its own, channels `threads` apart.
+enum : int { kSingle = 0, kVectors = 1, kHalves = 2 };
+template <int kMode>
 struct Own {
-  static constexpr bool vec = kAligned;
+  static constexpr int mode = kMode;
+  static constexpr bool vec = kMode != kSingle;
   int32_t me, threads, C;
-  __device__ __forceinline__ int32_t first(int j) const { return (me + j * threads) * kVec; }     // aligned rows
-  __device__ __forceinline__ int32_t one(int j, int i) const {
-    return vec ? first(j) + i : me + (j * kVec + i) * threads;
+  // first channel of half u of vector j (aligned rows)
+  __device__ __forceinline__ int32_t first(int j, int u) const {
+    return kMode == kVectors ? (me + j * threads) * kVec + 4 * u : (me + (2 * j + u) * threads) * 4;
   }
-  // some channel of vector j exists (aligned rows: all or none)
-  __device__ __forceinline__ bool any(int j) const { return (vec ? first(j) : me + j * kVec * threads) < C; }
+  __device__ __forceinline__ bool has(int j, int u) const { return first(j, u) < C; }
+  __device__ __forceinline__ int32_t one(int j, int i) const {
+    return vec ? first(j, i / 4) + i % 4 : me + (j * kVec + i) * threads;
+  }
+  // some channel of vector j exists
+  __device__ __forceinline__ bool any(int j) const { return (vec ? first(j, 0) : me + j * kVec * threads) < C; }
 };
 
 // This thread's share of a row of T on its way into its own ring slots (slot stride: `threads`
@@ -194,10 +207,16 @@ struct Fetch {
     if constexpr (O::vec) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (o.first(j) >= o.C) continue;
+        if constexpr (O::mode == kVectors && U == 1) {
+          if (o.has(j, 0)) cp_async16(ring + j * o.threads, row + o.first(j, 0));
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          cp_async16(ring + (j * U + u) * o.threads, reinterpret_cast<const uint4*>(row + o.first(j)) + u);
+          for (int u = 0; u < 2; ++u) {
+            if (!o.has(j, u)) continue;
+            if constexpr (U == 2) cp_async16(ring + (2 * j + u) * o.threads, row + o.first(j, u));
+            else cp_async8(reinterpret_cast<uint2*>(ring + j * o.threads) + u, row + o.first(j, u));
+          }
+        }
       }
     } else {
 #pragma unroll
@@ -231,6 +250,7 @@ __device__ __forceinline__ void read_vec(const uint4* ring, int j, const O& o, f
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) f[i] = 0ull;
   }
+  if (O::mode == kHalves && !o.has(j, 1)) f[2] = f[3] = 0ull;
 }
 
 template <typename T, typename O>
@@ -239,9 +259,15 @@ __device__ __forceinline__ void store_vec(T* row, int j, const O& o, const f2* f
   uint4 tmp[U];
   pack<T>(f, tmp);
   const T* p = reinterpret_cast<const T*>(tmp);
-  if (o.vec) {
+  if constexpr (O::mode == kVectors && U == 1) {
+    *reinterpret_cast<uint4*>(row + o.first(j, 0)) = tmp[0];
+  } else if constexpr (O::vec) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) reinterpret_cast<uint4*>(row + o.first(j))[u] = tmp[u];
+    for (int u = 0; u < 2; ++u) {
+      if (!o.has(j, u)) continue;
+      if constexpr (U == 2) *reinterpret_cast<uint4*>(row + o.first(j, u)) = tmp[u];
+      else *reinterpret_cast<uint2*>(row + o.first(j, u)) = reinterpret_cast<const uint2*>(tmp)[u];
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
@@ -254,15 +280,23 @@ __device__ __forceinline__ void store_vec(T* row, int j, const O& o, const f2* f
 template <typename T, int NV, typename O>
 __device__ __forceinline__ void param_values(const T* p, bool vec, const O& o, float (*f)[kVec]) {
   constexpr int U = units_of<T>();
-  if (vec && o.vec) {
+  if (vec && O::vec) {
     uint4 raw[NV][U];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        raw[j][u] = make_uint4(0, 0, 0, 0);
-        if (o.first(j) < o.C) raw[j][u] = __ldg(reinterpret_cast<const uint4*>(p + o.first(j)) + u);
+      for (int u = 0; u < U; ++u) raw[j][u] = make_uint4(0, 0, 0, 0);
+      if constexpr (O::mode == kVectors && U == 1) {
+        if (o.has(j, 0)) raw[j][0] = __ldg(reinterpret_cast<const uint4*>(p + o.first(j, 0)));
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (!o.has(j, u)) continue;
+          if constexpr (U == 2) raw[j][u] = __ldg(reinterpret_cast<const uint4*>(p + o.first(j, u)));
+          else reinterpret_cast<uint2*>(raw[j])[u] = __ldg(reinterpret_cast<const uint2*>(p + o.first(j, u)));
+        }
       }
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const T* t = reinterpret_cast<const T*>(raw[j]);
@@ -334,14 +368,14 @@ __device__ __forceinline__ Slice slice_of(const Args& a) {
 // Forward. TI: type of x; TO: type of y and of the residual. At least two CTAs share an SM, so that
 // one's barriers hide behind the other's work (64 registers at 512 threads, 128 at 256).
 // ------------------------------------------------------------------------------------
-template <typename TI, typename TO, int NV, bool kWarp, bool kAligned>
+template <typename TI, typename TO, int NV, bool kWarp, int kMode>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : NV == 4 ? 256 : kMaxThreads, 2)
 norm_fwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
   __shared__ __align__(16) float red[2][1][kMaxWarps];
   constexpr int UI = units_of<TI>(), UO = units_of<TO>();
   const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
-  const Own<kAligned> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
+  const Own<kMode> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
   const bool has_res = a.res != nullptr;
   const int stage_units = NV * (UI + (has_res ? UO : 0)) * threads;
   uint4* ring = ring_base + (kWarp ? (threadIdx.x >> 5) * a.stages * stage_units : 0) + o.me;
@@ -359,8 +393,8 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
   y += first * a.yn;
   const int64_t xstep = step * a.xn, rstep = step * a.rn, ystep = step * a.yn;
   int32_t next = first;
-  Fetch<TI, NV, Own<kAligned>> fx;
-  Fetch<TO, NV, Own<kAligned>> fr;
+  Fetch<TI, NV, Own<kMode>> fx;
+  Fetch<TO, NV, Own<kMode>> fr;
   auto start = [&](uint4* slot) {
     if (next < s.hi) {
       fx.start(slot, x, o);
@@ -440,7 +474,8 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
       for (int j = 0; j < NV; ++j) {
         if (!o.any(j)) continue;                   // what the thread does not own stays 0
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) v[j][i] = add2(v[j][i], sub);
+        for (int i = 0; i < kPairs; ++i)
+          if (o.mode != kHalves || i < 2 || o.has(j, 1)) v[j][i] = add2(v[j][i], sub);
         if (!o.vec) {
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) {
@@ -494,14 +529,14 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
 // sums, from the ring (whose slot is not refilled before the next row) instead of being held.
 // kBound: most threads of the CTA; 320 (up to 5,120 channels) leaves room for two CTAs an SM.
 // ------------------------------------------------------------------------------------
-template <typename TI, typename TO, int NV, bool kWarp, int kBound, bool kAligned>
+template <typename TI, typename TO, int NV, bool kWarp, int kBound, int kMode>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kBound, (kBound == kMaxThreads && NV > 1) || (kWarp && NV == 4) ? 1 : 2)
 norm_bwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
   __shared__ __align__(16) float red[2][2][kMaxWarps];
   constexpr int UI = units_of<TI>(), UO = units_of<TO>();
   const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
-  const Own<kAligned> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
+  const Own<kMode> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
   const bool has_res = a.res != nullptr;
   const int stage_units = NV * (UI + UO + (has_res ? UI : 0)) * threads;
   uint4* ring = ring_base + (kWarp ? (threadIdx.x >> 5) * a.stages * stage_units : 0) + o.me;
@@ -521,8 +556,8 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
   dx += first * a.yn;
   const int64_t xstep = step * a.xn, dstep = step * a.dn, rstep = step * a.rn, ystep = step * a.yn;
   int32_t next = first;
-  Fetch<TI, NV, Own<kAligned>> fx, fr;
-  Fetch<TO, NV, Own<kAligned>> fd;
+  Fetch<TI, NV, Own<kMode>> fx, fr;
+  Fetch<TO, NV, Own<kMode>> fd;
   auto start = [&](uint4* slot) {
     if (next < s.hi) {
       fx.start(slot, x, o);

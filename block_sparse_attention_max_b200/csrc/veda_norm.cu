@@ -77,13 +77,20 @@ Kernel by_types(int32_t ti, int32_t to) {
   if (ti == VEDA_BF16 && to == VEDA_FP32) return K<B, float>::kernel();
   return nullptr;
 }
+// A: aligned rows; who owns what there depends on the types
+template <typename TI, typename TO, bool A>
+constexpr int mode_of() { return !A ? norm::kSingle : sizeof(TI) == 4 || sizeof(TO) == 4 ? norm::kHalves : norm::kVectors; }
 template <int NV, bool W, bool A>
 struct Fwd {
-  template <typename TI, typename TO> struct K { static Kernel kernel() { return norm::norm_fwd_kernel<TI, TO, NV, W, A>; } };
+  template <typename TI, typename TO> struct K {
+    static Kernel kernel() { return norm::norm_fwd_kernel<TI, TO, NV, W, mode_of<TI, TO, A>()>; }
+  };
 };
 template <int NV, bool W, int BOUND, bool A>
 struct Bwd {
-  template <typename TI, typename TO> struct K { static Kernel kernel() { return norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, A>; } };
+  template <typename TI, typename TO> struct K {
+    static Kernel kernel() { return norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, mode_of<TI, TO, A>()>; }
+  };
 };
 constexpr int kMid = 320, kBig = norm::kMaxThreads;      // thread bounds of the CTA-per-row backward
 
