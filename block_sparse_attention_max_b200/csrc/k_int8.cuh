@@ -43,45 +43,38 @@ struct QuantArgs {
 
 constexpr int kQuantWarpK = 1024;
 constexpr int kQuantMaxK = 8192;      // ring kernels
-constexpr int kQuantVecs = 4;         // vectors a thread
+constexpr int kQuantVecs = 4;         // vectors a thread (a CTA per row with 8: 109 us where 4 take 86)
 constexpr int kQuantThreads = 256;    // most threads of a CTA
 constexpr int kQuantStages = 3;
 
-// x / s to the nearest integer, ties to even, |x| <= 127.5 s, for a quotient near a half-integer
-// (x * inv is off by less than 2^-15): fma rounds x - s (q +- 1/2) once, so its sign is exact.
-__device__ __forceinline__ int32_t div_round(float x, float s, float inv) {
-  float q = rintf(x * inv);
-  const float up = fmaf(-s, q + 0.5f, x), dn = fmaf(-s, q - 0.5f, x);
-  const bool odd = (static_cast<int32_t>(q) & 1) != 0;
-  if (up > 0.f || (up == 0.f && odd)) q += 1.f;
-  else if (dn < 0.f || (dn == 0.f && odd)) q -= 1.f;
-  return static_cast<int32_t>(q);
-}
-
-// The eight codes of a vector by the exact test (out of line: it runs rarely).
-__device__ __noinline__ uint2 codes8_exact(float4 a, float4 b, float s, float inv) {
-  const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= (static_cast<uint32_t>(div_round(f[i], s, inv)) & 0xffu) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
-}
-
 // Eight codes. Adding 1.5 * 2^23 to x * inv rounds it to an integer, ties to even, whose low byte
-// is the float's; d is what was rounded away. Only where some |d| is within 2^-14 of a half can an
-// integer be the wrong neighbour, and only then (1 vector in 500 or so) is the exact test run.
+// is the float's; d is what was rounded away. x * inv is off by less than 2^-15, so only where |d| is
+// within 2^-14 of a half can the integer be the wrong neighbour (16-bit inputs meet such borders, most
+// of them exact ties, once in 900 values): there fma rounds x - s (q +- 1/2) once, so its sign is exact.
 __device__ __forceinline__ uint2 codes8(const float* f, float s, float inv, bool live) {
   if (!live) return make_uint2(0u, 0u);
-  constexpr float kRound = 12582912.0f;
-  float t[8];
+  constexpr float kRound = 12582912.0f, kNear = 0.5f - 0x1p-14f;
+  const uint64_t inv2 = f2_splat(inv), round2 = f2_splat(kRound), minus2 = f2_splat(-1.0f);
+  float t[8], d[8];
   float worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t[i] = fmaf(f[i], inv, kRound);
-    worst = fmaxf(worst, fabsf(fmaf(f[i], inv, kRound - t[i])));
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t x = f2_pack(__float_as_uint(f[i]), __float_as_uint(f[i + 1]));
+    const uint64_t r = f2_fma(x, inv2, round2);
+    f2_unpack(r, t[i], t[i + 1]);
+    f2_unpack(f2_fma(x, inv2, f2_fma(r, minus2, round2)), d[i], d[i + 1]);
+    worst = fmax3(worst, fabsf(d[i]), fabsf(d[i + 1]));
   }
-  if (worst > 0.5f - 0x1p-14f)
-    return codes8_exact(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]), s, inv);
+  if (worst > kNear) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (fabsf(d[i]) <= kNear) continue;
+      const float h = copysignf(0.5f, d[i]);
+      const float z = fmaf(-s, (t[i] - kRound) + h, f[i]);            // x past the border q + h?
+      const bool odd = (__float_as_uint(t[i]) & 1u) != 0;
+      if ((h > 0.f ? z > 0.f : z < 0.f) || (z == 0.f && odd)) t[i] += 2.f * h;
+    }
+  }
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -104,16 +97,28 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits, bool& live) {
   return __fdiv_rn(amax, 127.0f);
 }
 
-// Largest |x| of a vector, as bits (packed for the 16-bit types, whose order is their bits').
-template <typename T> struct AbsMax {
-  uint32_t m = 0u;
+// Largest |x| of the vectors added, as fp32 bits, NaN above all.
+template <typename T> struct AbsMax;
+template <> struct AbsMax<__nv_bfloat16> {
+  __nv_bfloat162 m = __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
   __device__ __forceinline__ void add(const uint4& v) {
-    const uint32_t mask = 0x7fff7fffu;
-    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & mask, v.y & mask), __vmaxu2(v.z & mask, v.w & mask)));
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2_nan(m, __habs2(p[i]));
   }
   __device__ __forceinline__ uint32_t bits() const {
-    const uint16_t b = static_cast<uint16_t>(max(m & 0xffffu, m >> 16));
-    return __float_as_uint(rotary::Vec<T>::one(*reinterpret_cast<const T*>(&b))) & 0x7fffffffu;
+    return __float_as_uint(__bfloat162float(__hmax_nan(m.x, m.y))) & 0x7fffffffu;
+  }
+};
+template <> struct AbsMax<__half> {
+  __half2 m = __half2(__ushort_as_half(0), __ushort_as_half(0));
+  __device__ __forceinline__ void add(const uint4& v) {
+    const __half2* p = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2_nan(m, __habs2(p[i]));
+  }
+  __device__ __forceinline__ uint32_t bits() const {
+    return __float_as_uint(__half2float(__hmax_nan(m.x, m.y))) & 0x7fffffffu;
   }
 };
 template <> struct AbsMax<float> {
@@ -127,80 +132,100 @@ template <> struct AbsMax<float> {
 
 // kWarp: a row per warp, else a row per CTA. Rows start on 16-byte boundaries.
 template <typename T, bool kWarp>
-__global__ void __launch_bounds__(kQuantThreads) quant_ring_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : kWarp ? 3 : 4) quant_ring_kernel(const QuantArgs a) {
+  constexpr int kWarps = kQuantThreads / 32;
   using V = rotary::Vec<T>;
   constexpr int U = 8 / V::E;                                  // 16-byte units a vector
   constexpr int kStage = kQuantVecs * U;                       // units a thread and row
   extern __shared__ __align__(16) uint8_t quant_smem[];
-  __shared__ uint32_t red[2][kQuantThreads / 32];
+  __shared__ uint32_t red[2][kWarps];
   const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
   const int32_t me = kWarp ? (threadIdx.x & 31) : threadIdx.x, warps = blockDim.x >> 5;
   uint4* ring = reinterpret_cast<uint4*>(quant_smem) + (kWarp ? (threadIdx.x >> 5) * kQuantStages * kStage * 32 : 0) + me;
+  if (!kWarp) {
+    if (threadIdx.x < 2 * kWarps) (&red[0][0])[threadIdx.x] = 0u;
+    __syncthreads();
+  }
   const int64_t step = kWarp ? static_cast<int64_t>(gridDim.x) * warps : gridDim.x;
   const int64_t first = kWarp ? static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5) : blockIdx.x;
 
-  const auto fetch = [&](int64_t row, int st) {
-    if (row < a.rows) {
-      const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-      uint4* slot = ring + st * kStage * threads;
+  // first value of 16-byte unit u of vector j: a vector is 8 neighbouring values of a 16-bit type, or two
+  // fp32 units `threads` apart, so that a warp's accesses are contiguous
+  const auto unit = [&](int j, int u) { return (me + (j * U + u) * threads) * V::E; };
+  const T* x = static_cast<const T*>(a.x) + first * a.x_stride;     // the next row to fetch
+  const int64_t x_step = step * a.x_stride;
+  int64_t next = first;
+  const auto fetch = [&](uint4* slot) {
+    if (next < a.rows) {
 #pragma unroll
-      for (int j = 0; j < kQuantVecs; ++j) {
-        const int32_t k0 = (me + j * threads) * 8;
-        if (k0 + 8 <= a.K) {
+      for (int j = 0; j < kQuantVecs; ++j)
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            rotary::copy16_async(smem_u32(slot + (j * U + u) * threads), reinterpret_cast<const uint4*>(x + k0) + u);
-        } else if (k0 < a.kp) {                                // the row's end: zeros behind K
-          uint4 tmp[U];
-          T* t = reinterpret_cast<T*>(tmp);
+        for (int u = 0; u < U; ++u) {
+          const int32_t k0 = unit(j, u);
+          uint4* const to = slot + (j * U + u) * threads;
+          if (k0 + V::E <= a.K) {
+            rotary::copy16_async(smem_u32(to), x + k0);
+          } else if (k0 < a.kp) {                              // the row's end: zeros behind K
+            uint4 tmp;
+            T* t = reinterpret_cast<T*>(&tmp);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = k0 + i < a.K ? x[k0 + i] : V::to(0.f);
-#pragma unroll
-          for (int u = 0; u < U; ++u) slot[(j * U + u) * threads] = tmp[u];
+            for (int i = 0; i < V::E; ++i) t[i] = k0 + i < a.K ? x[k0 + i] : V::to(0.f);
+            *to = tmp;
+          }
         }
-      }
     }
     rotary::copies_commit();
+    x += x_step;
+    next += step;
   };
-  for (int i = 0; i < kQuantStages - 1; ++i) fetch(first + i * step, i);
-  int st = 0, flip = 0;
-  for (int64_t row = first; row < a.rows; row += step) {
+  const int32_t row_units = kStage * threads;
+  uint4* const ring_end = ring + kQuantStages * row_units;
+  uint4* free_slot = ring;
+  for (int i = 0; i < kQuantStages - 1; ++i, free_slot += row_units) fetch(free_slot);
+  uint4* slot = ring;
+  int flip = 0;
+  int8_t* out = a.codes + first * a.kp;
+  const int64_t out_step = step * a.kp;
+  for (int64_t row = first; row < a.rows; row += step, out += out_step) {
     rotary::copies_wait<kQuantStages - 2>();
-    const uint4* slot = ring + st * kStage * threads;
     uint4 raw[kQuantVecs][U];
     AbsMax<T> big;
 #pragma unroll
-    for (int j = 0; j < kQuantVecs; ++j) {
-      const bool own = (me + j * threads) * 8 < a.kp;
+    for (int j = 0; j < kQuantVecs; ++j)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        raw[j][u] = own ? slot[(j * U + u) * threads] : make_uint4(0, 0, 0, 0);
+        raw[j][u] = unit(j, u) < a.kp ? slot[(j * U + u) * threads] : make_uint4(0, 0, 0, 0);
         big.add(raw[j][u]);
       }
-    }
-    fetch(row + (kQuantStages - 1) * step, st == 0 ? kQuantStages - 1 : st - 1);   // read last round
+    fetch(free_slot);                                          // read in the previous round
     uint32_t m = __reduce_max_sync(0xffffffffu, big.bits());
     if (!kWarp) {
       if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = m;
       __syncthreads();
-      for (int32_t w = 0; w < warps; ++w) m = max(m, red[flip][w]);
+#pragma unroll
+      for (int32_t w = 0; w < kWarps; ++w) m = max(m, red[flip][w]);      // zeros past the last warp
       flip ^= 1;
     }
     bool live;
     const float s = row_scale(m, live);
     const float inv = 1.0f / s;
-    int8_t* out = a.codes + row * a.kp;
 #pragma unroll
     for (int j = 0; j < kQuantVecs; ++j) {
-      const int32_t k0 = (me + j * threads) * 8;
-      if (k0 >= a.kp) continue;
+      if (unit(j, 0) >= a.kp) continue;
       float f[8];
 #pragma unroll
       for (int u = 0; u < U; ++u) V::get(raw[j][u], f + u * V::E);
-      *reinterpret_cast<uint2*>(out + k0) = codes8(f, s, inv, live);
+      const uint2 q = codes8(f, s, inv, live);
+      if constexpr (U == 1) {
+        *reinterpret_cast<uint2*>(out + unit(j, 0)) = q;
+      } else {
+        *reinterpret_cast<uint32_t*>(out + unit(j, 0)) = q.x;
+        if (unit(j, 1) < a.kp) *reinterpret_cast<uint32_t*>(out + unit(j, 1)) = q.y;
+      }
     }
     if (me == 0) a.scale[row] = s;
-    st = st == kQuantStages - 1 ? 0 : st + 1;
+    free_slot = slot;
+    slot = slot + row_units == ring_end ? ring : slot + row_units;
   }
   rotary::copies_wait<0>();
 }

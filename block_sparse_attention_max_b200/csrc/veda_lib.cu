@@ -330,18 +330,18 @@ veda_status launch_rotary_tiles(rotary::TileArgs& p, bool half_layout, bool gath
   return launched("rotary_tiles_kernel");
 }
 
-// The ring kernels for aligned rows of up to 8,192 values: as many CTAs as stay resident (their
-// rings of 3 rows, at most 96 KB of fp32, and 64 to 96 registers a thread).
+// The ring kernels for aligned rows of up to 8,192 values: as many CTAs as stay resident beside their
+// rings of three rows.
 template <typename T>
 void launch_quant(const int8::QuantArgs& a, int sms, cudaStream_t s) {
-  constexpr int kRowUnits = int8::kQuantVecs * 8 * static_cast<int>(sizeof(T)) * int8::kQuantStages;   // bytes a thread
+  constexpr int NV = int8::kQuantVecs, kThreadBytes = NV * 8 * static_cast<int>(sizeof(T)) * int8::kQuantStages;
   if (a.vec && a.kp <= int8::kQuantWarpK) {
     const int64_t ctas = (a.rows + 7) / 8;
-    int8::quant_ring_kernel<T, true><<<grid_for(ctas, sms, sizeof(T) == 4 ? 2 : 4), 256, 256 * kRowUnits, s>>>(a);
+    int8::quant_ring_kernel<T, true><<<grid_for(ctas, sms, sizeof(T) == 4 ? 2 : 3), 256, 256 * kThreadBytes, s>>>(a);
   } else if (a.vec && a.kp <= int8::kQuantMaxK) {
-    const int threads = ((a.kp + 8 * int8::kQuantVecs - 1) / (8 * int8::kQuantVecs) + 31) / 32 * 32;
-    const int per_sm = std::min(sizeof(T) == 4 ? 512 / threads : 1024 / threads, 8);
-    int8::quant_ring_kernel<T, false><<<grid_for(a.rows, sms, per_sm), threads, threads * kRowUnits, s>>>(a);
+    const int threads = ((a.kp + 8 * NV - 1) / (8 * NV) + 31) / 32 * 32;
+    const int per_sm = (sizeof(T) == 4 ? 512 : 1024) / threads;
+    int8::quant_ring_kernel<T, false><<<grid_for(a.rows, sms, std::min(per_sm, 12)), threads, threads * kThreadBytes, s>>>(a);
   } else {
     int8::quant_row_kernel<T><<<grid_for(a.rows, sms, 8), int8::kQuantThreads, 0, s>>>(a);
   }
