@@ -285,6 +285,8 @@ veda_status host_device(int& sms) { return current_device(sms); }
 using namespace veda;
 
 namespace {
+constexpr int32_t kMaxInt8Rows = 1 << 30;      // tile coordinates stay 32-bit
+
 veda_status check_int8_product(const char* call, const void* a, const float* a_scale, const void* w, const float* w_scale,
                                const float* bias, const void* y, int64_t y_stride, int32_t dtype, int32_t M, int32_t N) {
   if (!a || !a_scale || !w || !w_scale || !y || !aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) ||
@@ -1129,7 +1131,7 @@ veda_status veda_rotary_unpermute(const void* x_tiled, void* x, const float* cos
 veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t dtype, void* codes, float* scale, int64_t rows,
                                int32_t K, veda_stream_t stream) {
   return guarded("veda_quantize_int8", [&]() -> veda_status {
-    if (rows < 0 || rows > INT32_MAX || K <= 0 || K > INT32_MAX - 16 || !known_type(dtype))
+    if (rows < 0 || rows > INT32_MAX || K <= 0 || K > (1 << 30) || !known_type(dtype))
       return fail(VEDA_ERR_INVALID_ARG, "veda_quantize_int8: bad size or type");
     if (rows == 0) return VEDA_OK;
     const int64_t es = type_size(dtype);
@@ -1155,6 +1157,7 @@ veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w,
     if (M < 0 || N < 0 || K <= 0 || !known_type(dtype) || y_stride < 0)
       return fail(VEDA_ERR_INVALID_ARG, "veda_int8_matmul: bad size or type");
     if (K > 131071) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_matmul: K above 131071 overflows the integer sum");
+    if (M > kMaxInt8Rows || N > kMaxInt8Rows) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_matmul: more than 2^30 rows");
     if (M == 0 || N == 0) return VEDA_OK;
     const int64_t es = type_size(dtype);
     veda_status st = check_int8_product("veda_int8_matmul", a, a_scale, w, w_scale, bias, y, y_stride, dtype, M, N);
@@ -1189,6 +1192,7 @@ veda_status veda_int8_linear(const void* x, int64_t x_stride, int32_t x_dtype, c
     if (M < 0 || N < 0 || K <= 0 || !known_type(x_dtype) || !known_type(y_dtype) || y_stride < 0)
       return fail(VEDA_ERR_INVALID_ARG, "veda_int8_linear: bad size or type");
     if (K > 131071) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_linear: K above 131071 overflows the integer sum");
+    if (M > kMaxInt8Rows || N > kMaxInt8Rows) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_linear: more than 2^30 rows");
     if (M == 0 || N == 0) return VEDA_OK;
     const int64_t kp = (static_cast<int64_t>(K) + 15) / 16 * 16, es = type_size(x_dtype);
     veda_status st;

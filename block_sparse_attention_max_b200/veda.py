@@ -1300,15 +1300,16 @@ class HostPipeline:
     and the device-to-host copy of clip i - 1's output (the host link carries both directions
     at once). Device copies of the raster inputs and of the raster output are kept per slot
     (``depth`` slots); CUDA events order every reuse of a slot after the work that last read
-    it, so a clip's result does not depend on its neighbours. ``synchronize`` waits for every
-    submitted clip's output to be in its host tensor.
+    it, so a clip's result does not depend on its neighbours. ``rotary``: positions for Q and K of
+    every clip. ``synchronize`` waits for every submitted clip's output to be in its host tensor.
     """
 
     def __init__(self, B: int, N: int, H: int, maps: DeviceMaps, rho: Sequence[Tuple[int, int]],
-                 scale: float, device, depth: int = 2):
+                 scale: float, device, depth: int = 2, rotary: Optional[RotaryTable] = None):
         if depth < 1:
             raise ValueError("depth must be >= 1")
         self.maps, self.rho, self.scale, self.depth = maps, list(rho), float(scale), depth
+        self.rotary = rotary
         bf = dict(dtype=torch.bfloat16, device=device)
         f32 = dict(dtype=torch.float32, device=device)
         self.inputs = [dict(q=torch.empty((B, N, H, 128), **bf), k=torch.empty((B, N, H, 128), **bf),
@@ -1341,7 +1342,7 @@ class HostPipeline:
             self.comp.wait_event(self.out_free[s])
         bufs = dataclasses.replace(self.bufs, o=self.outputs[s])
         sparse_attention(slot["q"], slot["k"], slot["v"], slot["wq"], slot["wk"], self.maps, self.rho,
-                         self.scale, buffers=bufs, stream=self.comp)
+                         self.scale, buffers=bufs, stream=self.comp, rotary=self.rotary)
         self.in_free[s].record(self.comp)
         self.out_ready[s].record(self.comp)
         # the output of slot s to the host

@@ -647,6 +647,7 @@ VEDA_API veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, cons
  *   codes    [rows][kp] int8 (device, out), kp = K rounded up to a multiple of 16, zeros behind
  *            K; 16-byte aligned
  *   scale    [rows] fp32 (device, out)
+ * Limits: K <= 2^30, rows < 2^31.
  */
 VEDA_API veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t dtype, void* codes,
                                         float* scale, int64_t rows, int32_t K, veda_stream_t stream);
@@ -658,7 +659,7 @@ VEDA_API veda_status veda_quantize_int8(const void* x, int64_t x_stride, int32_t
  *   a, w      [M][kp], [N][kp] int8 codes as veda_quantize_int8 stores them, 16-byte aligned
  *   bias      NULL or [N] fp32
  *   y         [M][N] of `dtype` (device, out), rows y_stride elements apart
- * Limits: K <= 131071 (128 * 128 * K stays below 2^31).
+ * Limits: K <= 131071 (128 * 128 * K stays below 2^31), M, N <= 2^30. The codes behind K must be 0.
  */
 VEDA_API veda_status veda_int8_matmul(const void* a, const float* a_scale, const void* w, const float* w_scale,
                                       const float* bias, void* y, int64_t y_stride, int32_t dtype, int32_t M,

@@ -112,7 +112,7 @@ def test_norm_workspace_covers_every_slice_count(L):
 def test_int8_refusals(L):
     q = lambda x=256, st=64, dt=0, c=16, s=16, rows=4, K=64: L.veda_quantize_int8(x, st, dt, c, s, rows, K, None)
     for bad in (dict(x=None), dict(c=None), dict(s=None), dict(c=8), dict(s=2), dict(x=255), dict(dt=3), dict(rows=-1),
-                dict(rows=2**31), dict(K=0), dict(K=2**31 - 8)):
+                dict(rows=2**31), dict(K=0), dict(K=2**30 + 1)):
         assert q(**bad) == INVALID, bad
     assert q(rows=0, x=None) == OK
 
@@ -122,7 +122,7 @@ def test_int8_refusals(L):
                 dict(sa=2), dict(sw=1), dict(bias=2), dict(y=17), dict(dt=4), dict(M=-1), dict(N=-1), dict(K=0),
                 dict(ys=31), dict(ys=-1)):
         assert mm(**bad) == INVALID, bad
-    assert mm(K=131072) == UNSUPPORTED
+    assert mm(K=131072) == mm(M=2**30 + 1) == mm(N=2**30 + 1, ys=2**31) == UNSUPPORTED
     assert mm(M=0) == OK and mm(N=0) == OK
 
     need = L.veda_int8_linear_workspace_bytes(9, 60)

@@ -182,3 +182,101 @@ def test_block_refuses_bad_shapes(V):
         V.rotary_permute_pool(q, short, maps)
     with pytest.raises(V.VedaError, match="rows"):
         V.rotary(q, short)
+
+
+def test_host_pipeline_with_positions(V):
+    w = synth.SMALL
+    maps, table = _setup(V, w)
+    scale = 1 / math.sqrt(128)
+    pipe = V.HostPipeline(w.B, w.N, w.H, maps, w.rho, scale, DEV, rotary=table)
+    pin = lambda t: t.cpu().pin_memory()
+    clips, outs = [], []
+    for i in range(3):
+        clips.append([pin(_rand(w.B, w.N, w.H, 128, seed=10 * i + j, dtype=torch.bfloat16)) for j in range(3)]
+                     + [pin(_rand(w.H, 128, 384, seed=10 * i + j, scale=0.02)) for j in (4, 5)])
+        outs.append(torch.empty((w.B, w.N, w.H, 128), dtype=torch.bfloat16).pin_memory())
+        pipe.submit(*clips[-1], outs[-1])
+    pipe.synchronize()
+    for c, o in zip(clips, outs):
+        ref = V.sparse_attention(*[t.to(DEV) for t in c], maps, w.rho, scale, rotary=table)
+        assert torch.equal(o, ref.o.cpu())
+
+
+def test_two_threads_on_their_own_streams(V):
+    """Calls enqueued from two host threads at once, each on its stream: bit for bit the results of
+    calls one after the other."""
+    import threading
+    N, C = 3000, 1280
+    f = V.rotary_frequencies(128)
+    table = V.rotary_table(torch.arange(N, device=DEV, dtype=torch.int32), f.inv_freq, f.axis)
+    wt = V.quantize_int8(_rand(640, C, seed=1))
+
+    def chain(seed, stream):
+        x, dy = _rand(1, N, C, seed=seed, dtype=torch.bfloat16), _rand(1, N, C, seed=seed + 1, dtype=torch.bfloat16)
+        sc = _rand(1, C, seed=seed + 2)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        out = []
+        for _ in range(4):
+            y, st = V.norm_modulate(x, sc, sc, want_stats=True, stream=stream)
+            g = V.norm_modulate_bwd(dy, x, st, sc, stream=stream)
+            r = V.rotary(y.view(1, N, C // 128, 128), table, stream=stream)
+            m = V.int8_linear(y, wt, stream=stream)
+            t = V.int8_linear(y[:, :40], wt, stream=stream)
+            out = [y, g.dx, g.dscale, g.dshift, r, m, t]
+        return out
+    serial = [chain(100 * i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def run(i):
+        torch.cuda.set_device(0)
+        s = torch.cuda.Stream()
+        got[i] = chain(100 * i, s)
+        s.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(serial, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_offsets_past_32_bits(V):
+    """Tensors of more than 2^31 elements: their last rows against calls on those rows alone."""
+    tail = 300
+    f = V.rotary_frequencies(128)
+    N, H = 140_000, 128
+    x = torch.empty((1, N, H, 128), device=DEV, dtype=torch.bfloat16)
+    assert x.numel() > 2**31
+    x[:, -tail:] = _rand(1, tail, H, 128, seed=1, dtype=torch.bfloat16)
+    x[:, :-tail] = 1
+    pos = torch.arange(N, device=DEV, dtype=torch.int32)
+    table = V.rotary_table(pos, f.inv_freq, f.axis)
+    y = V.rotary(x, table)
+    small = V.RotaryTable(table.cos_sin[-tail:].contiguous(), True)
+    assert torch.equal(y[:, -tail:], V.rotary(x[:, -tail:], small))
+    # the same memory as rows of 8,192 channels
+    rows = x.view(1, -1, 8192)
+    sc = _rand(1, 8192, seed=2)
+    h, st = V.norm_modulate(rows, sc, kind="rms", out=y.view(1, -1, 8192), want_stats=True)
+    n = tail * H * 128 // 8192
+    ref, st1 = V.norm_modulate(rows[:, -n:], sc, kind="rms", want_stats=True)
+    assert torch.equal(h[:, -n:], ref) and torch.equal(st.rstd[:, -n:], st1.rstd)
+    big = V.norm_modulate_bwd(rows, rows, st, sc, kind="rms", out=y.view(1, -1, 8192))
+    part = V.norm_modulate_bwd(rows[:, -n:], rows[:, -n:], st1, sc, kind="rms")
+    assert torch.equal(big.dx[:, -n:], part.dx)
+    del big, part, ref, h
+    q = V.quantize_int8(rows[0])
+    q1 = V.quantize_int8(rows[0, -n:])
+    assert torch.equal(q.codes[-n:], q1.codes) and torch.equal(q.scale[-n:], q1.scale)
+    del y, x, rows, q
+    # a product with more than 2^31 outputs
+    M, No, K = 70_000, 32_768, 48
+    a, w = V.quantize_int8(_rand(M, K, seed=3)), V.quantize_int8(_rand(No, K, seed=4))
+    out = V.int8_matmul(a, w)
+    assert out.numel() > 2**31
+    last = V.Int8Rows(a.codes[-300:].contiguous(), a.scale[-300:].contiguous(), K)
+    assert torch.equal(out[-300:], V.int8_matmul(last, w))
+    V.check_device_status()
