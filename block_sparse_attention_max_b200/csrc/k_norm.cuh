@@ -177,7 +177,9 @@ __device__ __forceinline__ float inv_sqrt(float v) {
 //   kHalves: every half is on its own, halves `threads` apart, so that the accesses of a warp to fp32
 //     rows are contiguous too (two 16-byte accesses a vector 32 bytes apart fetch every sector twice:
 //     58% of the HBM copy rate where this has 80%); 16-bit rows beside them move in 8-byte pieces;
-//   kSingle: rows without 16-byte boundaries: every channel on its own, channels `threads` apart.
+//   kSingle: rows without 16-byte boundaries: every channel on its own, channels `threads` apart; the
+//     CTA's size is a constant there (kFixed), as a channel's address would otherwise cost more than the
+//     channel's arithmetic (backward of 6,147 rows of 1,023: 33 us with a run-time size, 24 with this).
 enum : int { kSingle = 0, kVectors = 1, kHalves = 2 };
 template <int kMode>
 struct Own {
@@ -368,13 +370,13 @@ __device__ __forceinline__ Slice slice_of(const Args& a) {
 // Forward. TI: type of x; TO: type of y and of the residual. At least two CTAs share an SM, so that
 // one's barriers hide behind the other's work (64 registers at 512 threads, 128 at 256).
 // ------------------------------------------------------------------------------------
-template <typename TI, typename TO, int NV, bool kWarp, int kMode>
+template <typename TI, typename TO, int NV, bool kWarp, int kMode, int kFixed>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : NV == 4 ? 256 : kMaxThreads, 2)
 norm_fwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
   __shared__ __align__(16) float red[2][1][kMaxWarps];
   constexpr int UI = units_of<TI>(), UO = units_of<TO>();
-  const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
+  const int32_t threads = kWarp ? 32 : kFixed ? kFixed : static_cast<int32_t>(blockDim.x);
   const Own<kMode> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
   const bool has_res = a.res != nullptr;
   const int stage_units = NV * (UI + (has_res ? UO : 0)) * threads;
@@ -529,13 +531,14 @@ norm_fwd_kernel(const __grid_constant__ Args a) {
 // sums, from the ring (whose slot is not refilled before the next row) instead of being held.
 // kBound: most threads of the CTA; 320 (up to 5,120 channels) leaves room for two CTAs an SM.
 // ------------------------------------------------------------------------------------
-template <typename TI, typename TO, int NV, bool kWarp, int kBound, int kMode>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kBound, (kBound == kMaxThreads && NV > 1) || (kWarp && NV == 4) ? 1 : 2)
+template <typename TI, typename TO, int NV, bool kWarp, int kBound, int kMode, int kFixed>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : kFixed ? kFixed : kBound,
+                                  kFixed == 128 ? 5 : kBound == kMaxThreads || (kWarp && NV == 4) ? 1 : 2)
 norm_bwd_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint4 ring_base[];
   __shared__ __align__(16) float red[2][2][kMaxWarps];
   constexpr int UI = units_of<TI>(), UO = units_of<TO>();
-  const int32_t threads = kWarp ? 32 : static_cast<int32_t>(blockDim.x);
+  const int32_t threads = kWarp ? 32 : kFixed ? kFixed : static_cast<int32_t>(blockDim.x);
   const Own<kMode> o{kWarp ? static_cast<int32_t>(threadIdx.x & 31) : static_cast<int32_t>(threadIdx.x), threads, a.C};
   const bool has_res = a.res != nullptr;
   const int stage_units = NV * (UI + UO + (has_res ? UI : 0)) * threads;

@@ -47,8 +47,8 @@ constexpr int kMaxRing = 224 * 1024;
 //     are faster as long as their registers leave two CTAs an SM: forward without a residual 4
 //     (5,120: 78%; 2: 72%), with one 2 (8,192: 89%; 4: 78%), backward 2 (5,120: 80%; 4: 60%).
 // Rows without 16-byte boundaries are fetched with plain loads that stall their warp, so there more
-// warps with less each are faster: above 256 channels a CTA of 1-vector threads (backward of 6,147
-// rows of 1,023: 29 us; a warp a row 41 us).
+// warps with less each are faster: above 256 channels a CTA of 1-vector threads, of 128, 256 or 512
+// (backward of 6,147 rows of 1,023, a warp a row 41 us, 64 threads of 2 vectors 54 us).
 struct Shape {
   int nv;          // vectors per thread
   bool warp;       // a row per warp
@@ -59,7 +59,8 @@ Shape shape_of(int32_t C, bool is_aligned, bool bwd, bool res) {
   const int warp_threads = 32 * norm::kWarpsPerCta;
   if (C <= 256) return {1, true, warp_threads};
   if (is_aligned && C <= norm::kWarpCols) return {C <= 512 ? 2 : 4, true, warp_threads};
-  const int nv = is_aligned ? (bwd || res ? 2 : 4) : C <= 4096 ? 1 : 2;
+  if (!is_aligned) return {C <= 4096 ? 1 : 2, false, C <= 1024 ? 128 : C <= 2048 ? 256 : norm::kMaxThreads};
+  const int nv = bwd || res ? 2 : 4;
   return {nv, false, ((vecs + nv - 1) / nv + 31) / 32 * 32};     // at most kMaxThreads (nv 4: 256)
 }
 
@@ -80,16 +81,16 @@ Kernel by_types(int32_t ti, int32_t to) {
 // A: aligned rows; who owns what there depends on the types
 template <typename TI, typename TO, bool A>
 constexpr int mode_of() { return !A ? norm::kSingle : sizeof(TI) == 4 || sizeof(TO) == 4 ? norm::kHalves : norm::kVectors; }
-template <int NV, bool W, bool A>
+template <int NV, bool W, bool A, int FIXED = 0>
 struct Fwd {
   template <typename TI, typename TO> struct K {
-    static Kernel kernel() { return norm::norm_fwd_kernel<TI, TO, NV, W, mode_of<TI, TO, A>()>; }
+    static Kernel kernel() { return norm::norm_fwd_kernel<TI, TO, NV, W, mode_of<TI, TO, A>(), FIXED>; }
   };
 };
-template <int NV, bool W, int BOUND, bool A>
+template <int NV, bool W, int BOUND, bool A, int FIXED = 0>
 struct Bwd {
   template <typename TI, typename TO> struct K {
-    static Kernel kernel() { return norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, mode_of<TI, TO, A>()>; }
+    static Kernel kernel() { return norm::norm_bwd_kernel<TI, TO, NV, W, BOUND, mode_of<TI, TO, A>(), FIXED>; }
   };
 };
 constexpr int kMid = 320, kBig = norm::kMaxThreads;      // thread bounds of the CTA-per-row backward
@@ -98,9 +99,10 @@ constexpr int kMid = 320, kBig = norm::kMaxThreads;      // thread bounds of the
 Kernel pick(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to) {
   if (!is_aligned) {
     if (s.warp) return bwd ? by_types<Bwd<1, true, 256, false>::K>(ti, to) : by_types<Fwd<1, true, false>::K>(ti, to);
-    if (s.nv == 1) return bwd ? by_types<Bwd<1, false, kBig, false>::K>(ti, to) : by_types<Fwd<1, false, false>::K>(ti, to);
-    if (!bwd) return by_types<Fwd<2, false, false>::K>(ti, to);
-    return s.threads <= kMid ? by_types<Bwd<2, false, kMid, false>::K>(ti, to) : by_types<Bwd<2, false, kBig, false>::K>(ti, to);
+    if (s.nv == 2) return bwd ? by_types<Bwd<2, false, kBig, false, 512>::K>(ti, to) : by_types<Fwd<2, false, false, 512>::K>(ti, to);
+    if (s.threads == 128) return bwd ? by_types<Bwd<1, false, kBig, false, 128>::K>(ti, to) : by_types<Fwd<1, false, false, 128>::K>(ti, to);
+    if (s.threads == 256) return bwd ? by_types<Bwd<1, false, kBig, false, 256>::K>(ti, to) : by_types<Fwd<1, false, false, 256>::K>(ti, to);
+    return bwd ? by_types<Bwd<1, false, kBig, false, 512>::K>(ti, to) : by_types<Fwd<1, false, false, 512>::K>(ti, to);
   }
   if (s.warp) {
     if (s.nv == 1) return bwd ? by_types<Bwd<1, true, 256, true>::K>(ti, to) : by_types<Fwd<1, true, true>::K>(ti, to);
