@@ -150,16 +150,17 @@ veda_status resident(Kernel k, int threads, int bytes, int& per_sm) {
 }
 
 // Slices per sequence: together the CTAs that can run at once (so a CTA keeps its channels'
-// parameters for as many rows as possible), no more than there are rows.
-constexpr int kMaxPerSmFwd = 8, kMaxPerSmBwd = 4, kMaxSms = 160;
-veda_status slices_for(Kernel k, const Shape& s, int bytes, int sms, int cap, int32_t B, int32_t N, int32_t& slices) {
+// parameters for as many rows as possible), no more than there are rows; in the backward with a few
+// rows each, as every slice also writes two rows of fp32 sums.
+constexpr int kMaxPerSmFwd = 8, kMaxPerSmBwd = 4, kMaxSms = 160, kMinRowsBwd = 4;
+veda_status slices_for(Kernel k, const Shape& s, int bytes, int sms, bool bwd, int32_t B, int32_t N, int32_t& slices) {
   int per_sm = 0;
   const veda_status st = resident(k, s.threads, bytes, per_sm);
   if (st != VEDA_OK) return st;
-  per_sm = std::max(1, std::min(per_sm, cap));
+  per_sm = std::max(1, std::min(per_sm, bwd ? kMaxPerSmBwd : kMaxPerSmFwd));
   const int64_t want = (static_cast<int64_t>(std::min(sms, kMaxSms)) * per_sm + B - 1) / B;
-  const int64_t rows = s.warp ? (N + norm::kWarpsPerCta - 1) / norm::kWarpsPerCta : N;
-  slices = static_cast<int32_t>(std::max<int64_t>(1, std::min(want, rows)));
+  const int64_t rows = (s.warp ? norm::kWarpsPerCta : 1) * (bwd ? kMinRowsBwd : 1);       // a slice's, at least
+  slices = static_cast<int32_t>(std::max<int64_t>(1, std::min(want, N / rows + (bwd ? 0 : N % rows != 0))));
   return VEDA_OK;
 }
 
@@ -230,7 +231,7 @@ veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const v
     const Shape s = shape_of(C, vec, false, residual != nullptr);
     const int bytes = ring_bytes(s, false, vec, x->dtype, y->dtype, residual != nullptr, a.stages);
     const Kernel k = pick(s, false, vec, x->dtype, y->dtype);
-    if ((st = slices_for(k, s, bytes, sms, kMaxPerSmFwd, B, N, a.slices)) != VEDA_OK) return st;
+    if ((st = slices_for(k, s, bytes, sms, false, B, N, a.slices)) != VEDA_OK) return st;
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "norm_fwd_kernel");
@@ -297,7 +298,7 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     const int bytes = ring_bytes(s, true, vec, x->dtype, dy->dtype, a.res != nullptr, a.stages);
     a.part = static_cast<float*>(workspace);
     const Kernel k = pick(s, true, vec, x->dtype, dy->dtype);
-    if ((st = slices_for(k, s, bytes, sms, kMaxPerSmBwd, B, N, a.slices)) != VEDA_OK) return st;
+    if ((st = slices_for(k, s, bytes, sms, true, B, N, a.slices)) != VEDA_OK) return st;
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, s0>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "norm_bwd_kernel");

@@ -1000,21 +1000,17 @@ def _norm_bwd(dy, x, x3, stats, params, has, residual_grad, residual_scale, kind
         for t, n in ((x3, "x"), (dy3, "dy"), (res3, "residual_grad")):
             _separate(out3, t, n, True)
     gain, shift, weight, bias = has
-    # the gradients of the vectors are rows of one buffer: [B] gain, [B] shift, weight, bias
-    rows = B * gain + B * shift + weight + bias
-    vec = _new(x, (rows, C), torch.float32, stream)
-    take, at = [], 0
-    for want, n in ((gain, B), (shift, B), (weight, 1), (bias, 1)):
-        take.append(vec[at:at + n] if want else None)
-        at += n * want
-    dgain, dshift, dweight, dbias = take
+    f32 = torch.float32
+    dgain = _new(x, (B, C), f32, stream) if gain else None
+    dshift = _new(x, (B, C), f32, stream) if shift else None
+    dweight = _new(x, (C,), f32, stream) if weight else None
+    dbias = _new(x, (C,), f32, stream) if bias else None
     nbytes = lib().veda_norm_bwd_workspace_bytes(B, N, C)
     work = _new(x, (max(nbytes, 16),), torch.uint8, stream)
     _check("veda_norm_bwd", lib().veda_norm_bwd(
         _rows(dy3), _rows(x3), mean, rstd, _rows(res3), _rows(out3), params, residual_scale, _ptr(dgain),
         _ptr(dshift), _ptr(dweight), _ptr(dbias), work.data_ptr(), work.numel(), B, N, C, k, _stream(stream)))
-    one = lambda t: None if t is None else t[0]
-    return out, dgain, dshift, one(dweight), one(dbias)
+    return out, dgain, dshift, dweight, dbias
 
 
 def norm_modulate_bwd(dy: torch.Tensor, x: torch.Tensor, stats: Optional[NormStats],
