@@ -34,10 +34,18 @@ bool vec_rows(const void* p, int64_t sb, int64_t sn, int32_t dtype) {
   return on(p, 16) && sb * size_of(dtype) % 16 == 0 && sn * size_of(dtype) % 16 == 0;
 }
 
-// Rows in the ring: enough bytes in flight for the HBM's latency (Little's law asks for about
-// 45 KB an SM), fewer where a CTA's ring would not fit its share of shared memory.
-constexpr int kFwdStages = 4, kBwdStages = 3;
+// Rows in the ring: enough bytes in flight for the HBM's latency (Little's law asks for about 45 KB
+// an SM), few enough that several CTAs share the SM. Measured as below, of 2 / 3 / 4 rows: forward at
+// 5,120 channels, bf16 73 / 79 / 78%, with a residual 93 / 84 / 87% (two tensors: three CTAs an SM
+// with 2, two with 4; 256 channels, a row per warp, 77 / 91 / 85%), fp32 to bf16 87 / 88 / 72% (with 4
+// one CTA an SM), fp32 residual at 4,096 88 / 92 / 94%; backward 2: 78, 3: 79%.
 constexpr int kMaxRing = 224 * 1024;
+int ring_rows(bool bwd, bool is_aligned, int32_t ti, int32_t to, bool res, int32_t C) {
+  if (!is_aligned) return 2;                     // plain loads: one row ahead
+  if (bwd) return 3;
+  if (res) return ti != VEDA_FP32 && to != VEDA_FP32 && C > 512 ? 2 : 4;
+  return ti == VEDA_FP32 ? 3 : 4;
+}
 
 // Who holds a row. Measured on 120 M bf16 values (share of the HBM copy rate; forward without /
 // with a residual, backward):
@@ -45,7 +53,7 @@ constexpr int kMaxRing = 224 * 1024;
 //     1-vector threads there 58 / 84 / 63%;
 //   above, a CTA: the row sums cost a thread the same whatever it holds, so more vectors a thread
 //     are faster as long as their registers leave two CTAs an SM: forward without a residual 4
-//     (5,120: 78%; 2: 72%), with one 2 (8,192: 89%; 4: 78%), backward 2 (5,120: 80%; 4: 60%).
+//     (5,120: 78%; 2: 72%), with one 2 (8,192: 93%; 4: 78%), backward 2 (5,120: 80%; 4: 60%).
 // Rows without 16-byte boundaries are fetched with plain loads that stall their warp, so there more
 // warps with less each are faster: above 256 channels a CTA of 1-vector threads, of 128, 256 or 512
 // (backward of 6,147 rows of 1,023, a warp a row 41 us, 64 threads of 2 vectors 54 us).
@@ -114,11 +122,11 @@ Kernel pick(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to) {
 }
 
 // Ring bytes of a CTA: every row a group has in flight, 16-byte units.
-int ring_bytes(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to, bool res, int32_t& stages) {
+int ring_bytes(const Shape& s, bool bwd, bool is_aligned, int32_t ti, int32_t to, bool res, int32_t C, int32_t& stages) {
   const int ui = ti == VEDA_FP32 ? 2 : 1, uo = to == VEDA_FP32 ? 2 : 1;
   const int units = bwd ? ui + uo + (res ? ui : 0) : ui + (res ? uo : 0);
   const int row = s.nv * units * s.threads * 16;            // <= 96 KB (fp32, 8,192 channels)
-  stages = !is_aligned ? 2 : bwd ? kBwdStages : kFwdStages;   // plain loads: one row ahead
+  stages = ring_rows(bwd, is_aligned, ti, to, res, C);
   while (stages > 2 && stages * row > kMaxRing) --stages;
   return stages * row;
 }
@@ -229,7 +237,7 @@ veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const v
     const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.y, a.yb, a.yn, y->dtype) &&
             (!residual || vec_rows(a.res, a.rb, a.rn, y->dtype));
     const Shape s = shape_of(C, vec, false, residual != nullptr);
-    const int bytes = ring_bytes(s, false, vec, x->dtype, y->dtype, residual != nullptr, a.stages);
+    const int bytes = ring_bytes(s, false, vec, x->dtype, y->dtype, residual != nullptr, C, a.stages);
     const Kernel k = pick(s, false, vec, x->dtype, y->dtype);
     if ((st = slices_for(k, s, bytes, sms, false, B, N, a.slices)) != VEDA_OK) return st;
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, reinterpret_cast<cudaStream_t>(stream)>>>(a);
@@ -295,7 +303,7 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     const bool vec = C % norm::kVec == 0 && vec_rows(a.x, a.xb, a.xn, x->dtype) && vec_rows(a.dy, a.db, a.dn, dy->dtype) &&
             vec_rows(a.y, a.yb, a.yn, x->dtype) && (!a.res || vec_rows(a.res, a.rb, a.rn, x->dtype));
     const Shape s = shape_of(C, vec, true, a.res != nullptr);
-    const int bytes = ring_bytes(s, true, vec, x->dtype, dy->dtype, a.res != nullptr, a.stages);
+    const int bytes = ring_bytes(s, true, vec, x->dtype, dy->dtype, a.res != nullptr, C, a.stages);
     a.part = static_cast<float*>(workspace);
     const Kernel k = pick(s, true, vec, x->dtype, dy->dtype);
     if ((st = slices_for(k, s, bytes, sms, true, B, N, a.slices)) != VEDA_OK) return st;
