@@ -284,13 +284,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 // ------------------------------------------------------------------------------------
 // The tile kernels. A CTA takes one tile of up to 8 neighbouring heads, a warp a head; the tile's
 // 128 rows go by in batches of 8, and the batches of a CTA's tiles form one stream: while one is
-// turned and written, the next one's rows (each warp's own) and its rows of the table (one copy
-// for the CTA) are on their way into the other buffer by asynchronous copies, and the token indices
-// of the batch after that are on their way into a register.
+// turned and written, the next two batches' rows (each warp's own) and their rows of the table (one
+// copy for the CTA) are on their way into the other buffers by asynchronous copies, and the token
+// indices of the batch after those are on their way into a register.
 //
 // The table is what decides the speed: a token's row of it has rot_dim * 4 bytes, twice the 256
 // bytes of the row it turns. Read by every head from L2, 8 to 16 rows in registers at a time, the
-// gather of the 16:9 clip took 378 us a tensor. Neighbouring heads mostly have the same tile map,
+// gather of the 16:9 clip took 378 us a tensor; this one takes 224 (185 at the HBM copy rate; 240 with
+// one batch on its way instead of two). Neighbouring heads mostly have the same tile map,
 // so the CTA copies the rows of its first head's tokens once; a warp whose head has another token
 // in some slot (per-head tile orders) reads its rows of the table from global memory instead.
 //
@@ -312,6 +313,7 @@ struct TileArgs {
 
 constexpr int kTileHeads = 8;
 constexpr int kBatchRows = 8;
+constexpr int kTileBuffers = 3;
 // one buffer: hg warps' rows, then the table's rows
 __host__ __device__ constexpr uint32_t tile_buffer_bytes(int32_t hg, int32_t P) {
   return static_cast<uint32_t>(hg) * kBatchRows * kRowBytes + kBatchRows * static_cast<uint32_t>(P) * 8u;
@@ -351,20 +353,19 @@ __device__ __forceinline__ void unpack4(uint2 v, float* f) {
 
 // Place in a CTA's stream of batches.
 struct TileBatch {
-  int64_t u;
-  int32_t r0, b, h0, t;
-  __device__ __forceinline__ void at(int64_t unit, const TileArgs& p) {
+  int32_t u, r0, b, h0, t;
+  __device__ __forceinline__ void at(int32_t unit, const TileArgs& p) {
     u = unit;
     r0 = 0;
     if (u >= p.g.units) return;
-    const int64_t bt = u / p.groups;
-    h0 = static_cast<int32_t>(u - bt * p.groups) * p.hg;
-    b = static_cast<int32_t>(bt / p.g.nT);
-    t = static_cast<int32_t>(bt - static_cast<int64_t>(b) * p.g.nT);
+    const int32_t bt = u / p.groups;
+    h0 = (u - bt * p.groups) * p.hg;
+    b = bt / p.g.nT;
+    t = bt - b * p.g.nT;
   }
   __device__ __forceinline__ void advance(const TileArgs& p) {
     r0 += kBatchRows;
-    if (r0 == 128) at(u + gridDim.x, p);
+    if (r0 == 128) at(u + static_cast<int32_t>(gridDim.x), p);
   }
   // lanes r and 8 + r: token of slot r0 + r of head h0 + warp; lanes 16 + r and 24 + r: of head h0.
   // -1 where there is none (past the stream, past the heads, pad slots).
@@ -440,23 +441,29 @@ __global__ void __launch_bounds__(32 * kTileHeads, 3) rotary_tiles_kernel(const 
     copies_commit();
   };
 
+  // batches: the one at work, the next one (on its way), the one after (its tokens are known), and the
+  // one whose tokens are on their way
   TileBatch cur, nxt, far;
-  cur.at(blockIdx.x, p);
+  cur.at(static_cast<int32_t>(blockIdx.x), p);
   int32_t tok_cur = checked(cur.token(p, warp, lane));
   issue(cur, tok_cur, 0);
   nxt = cur;
   nxt.advance(p);
   int32_t tok_nxt = checked(nxt.token(p, warp, lane));
+  issue(nxt, tok_nxt, 1);
   far = nxt;
+  far.advance(p);
+  int32_t tok_far = checked(far.token(p, warp, lane));
   uint32_t k = 0;
   float sum[8], mx[8], mn[8];
   int32_t nv = 0;
   while (cur.u < a.units) {
-    far.advance(p);
-    const int32_t tok_far = far.token(p, warp, lane);
-    copies_wait<0>();
-    __syncthreads();            // the batch is here for the whole CTA, and the other buffer is free
-    issue(nxt, tok_nxt, k ^ 1);
+    TileBatch last = far;
+    last.advance(p);
+    const int32_t tok_last = last.token(p, warp, lane);
+    copies_wait<1>();
+    __syncthreads();            // the batch is here for the whole CTA, and the previous one's buffer is free
+    issue(far, tok_far, k == 0 ? 2 : k - 1);
     const int32_t h = cur.h0 + static_cast<int32_t>(warp);
     if (h < a.H) {
       if (kGather && cur.r0 == 0) {
@@ -620,8 +627,10 @@ __global__ void __launch_bounds__(32 * kTileHeads, 3) rotary_tiles_kernel(const 
     cur = nxt;
     tok_cur = tok_nxt;
     nxt = far;
-    tok_nxt = checked(tok_far);
-    k ^= 1;
+    tok_nxt = tok_far;
+    far = last;
+    tok_far = checked(tok_last);
+    k = k == 2 ? 0 : k + 1;
   }
   copies_wait<0>();
 }

@@ -36,7 +36,7 @@ struct DeviceInfo {
   int per_sm_copy = 1, per_sm_unpermute = 1, per_sm_pool = 1, per_sm_permpool = 1;   // resident CTAs per SM
 };
 constexpr int kMaxDevices = 64;
-static_assert(2 * rotary::tile_buffer_bytes(rotary::kTileHeads, 64) <= 48 * 1024, "no opt-in needed");
+constexpr int kRotaryTileSmem = rotary::kTileBuffers * static_cast<int>(rotary::tile_buffer_bytes(rotary::kTileHeads, 64));
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 
@@ -90,6 +90,14 @@ veda_status current_device(int& sms) {
         {reinterpret_cast<const void*>(bwd::bwd_kernel<bwd::kModeDKDV>), static_cast<int>(bwd::kSmemBytesDKDV)},
         {reinterpret_cast<const void*>(sgemm::nt_gemm_3xtf32_kernel), static_cast<int>(sgemm::kSmemBytes)},
         {reinterpret_cast<const void*>(select_kernel), static_cast<int>(kSelMaxSmem)},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<false, false, false>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<false, false, true>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<false, true, false>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<false, true, true>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<true, false, false>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<true, false, true>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<true, true, false>), kRotaryTileSmem},
+        {reinterpret_cast<const void*>(rotary::rotary_tiles_kernel<true, true, true>), kRotaryTileSmem},
         {reinterpret_cast<const void*>(int8::quant_ring_kernel<__nv_bfloat16, true>), 49152},
         {reinterpret_cast<const void*>(int8::quant_ring_kernel<__half, true>), 49152},
         {reinterpret_cast<const void*>(int8::quant_ring_kernel<float, true>), 98304},
@@ -320,8 +328,9 @@ veda_status launch_rotary_tiles(rotary::TileArgs& p, bool half_layout, bool gath
   p.groups = (p.g.H + rotary::kTileHeads - 1) / rotary::kTileHeads;
   p.hg = (p.g.H + p.groups - 1) / p.groups;
   p.g.units = static_cast<int64_t>(p.g.B) * p.g.nT * p.groups;
-  const uint32_t bytes = 2 * rotary::tile_buffer_bytes(p.hg, p.P);        // at most 40 KB
-  const int per_sm = std::min(24 / p.hg, static_cast<int>(200 * 1024 / bytes));
+  if (p.g.units > INT32_MAX / 2) return fail(VEDA_ERR_UNSUPPORTED, "rotary_tiles_kernel: too many tiles");
+  const uint32_t bytes = rotary::kTileBuffers * rotary::tile_buffer_bytes(p.hg, p.P);        // at most 60 KB
+  const int per_sm = std::min(24 / p.hg, static_cast<int>(216 * 1024 / bytes));
   typedef void (*Kernel)(const rotary::TileArgs);
   static const Kernel kernels[2][2][2] = {     // [half layout][gather][every channel turned]
       {{rotary::rotary_tiles_kernel<false, false, false>, rotary::rotary_tiles_kernel<false, false, true>},

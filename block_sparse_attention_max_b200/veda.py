@@ -141,7 +141,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -681,7 +681,9 @@ def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:
     """A buffer beside `like` for work on `stream` (None: the current one): taken from that stream's
     memory, and kept from reuse until what the current stream does with it later has run."""
     if stream is None:
-        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
+        if dtype is not like.dtype:
+            return like.new_empty(shape, dtype=dtype)
+        return torch.empty_like(like) if shape == like.shape and like.is_contiguous() else like.new_empty(shape)
     with torch.cuda.stream(stream):
         t = like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream())
@@ -768,6 +770,9 @@ class RotaryTable:
         return 2 * self.cos_sin.shape[1]
 
     def _check(self) -> None:
+        t = self.cos_sin
+        if t.dtype is torch.float32 and t.dim() == 3 and t.shape[2] == 2 and t.is_contiguous() and _here(t):
+            return
         if self.cos_sin.dim() != 3 or self.cos_sin.shape[2] != 2:
             raise ValueError("cos_sin: expected shape [rows, P, 2]")
         _need(self.cos_sin, torch.float32, "cos_sin")
