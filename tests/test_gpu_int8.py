@@ -41,7 +41,8 @@ def _check_rows(got, x):
 
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (9, 16), (17, 100), (5, 1024), (6, 1025), (3, 1032), (4, 4101),
-                                    (2, 5120), (3, 8192), (2, 8200), (2, 20001)])
+                                    (2, 5120), (3, 8192), (2, 8200), (2, 20001), (9000, 200),
+                                    (3000, 1040), (2500, 5120), (2000, 1025)])
 def test_quantize(V, dtype, rows, K):
     x = _rand(rows, K, seed=K, dtype=TYPES[dtype])
     _check_rows(V.quantize_int8(x), x)
@@ -101,7 +102,7 @@ def _product(a, sa, w, sw, bias):
 SIZES = [(1, 1, 1), (1, 5, 17), (1, 257, 5120), (2, 100, 333), (2, 3000, 64), (3, 127, 16), (4, 129, 5000), (7, 5200, 130),
          (17, 600, 1100), (33, 128, 2000), (65, 1000, 700), (100, 70, 4097), (128, 2049, 384), (3, 64, 48), (5, 1000, 640), (8, 130, 4101), (9, 1, 1),
          (9, 33, 50), (16, 256, 128), (31, 300, 127), (64, 511, 1040), (127, 255, 129), (128, 256, 512), (129, 257, 513),
-         (200, 640, 256), (300, 1030, 2064), (777, 515, 4101), (1000, 2600, 100), (2049, 96, 130)]
+         (200, 640, 256), (300, 1030, 2064), (777, 515, 4101), (1000, 2600, 100), (2049, 96, 130), (256, 5120, 200), (20000, 64, 256), (20000, 128, 384)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)

@@ -64,11 +64,14 @@ def _forward(x, kind, w, b, G, S, r, res, eps=EPS):
 
 
 SIZES = [(1, 1, 1), (2, 3, 8), (1, 7, 63), (3, 5, 128), (2, 9, 256), (1, 40, 264), (2, 6, 512), (2, 5, 1000),
-         (1, 65, 1023), (1, 11, 1024), (2, 3, 1032), (1, 33, 4096), (1, 9, 5120), (1, 4, 5121), (1, 3, 7168), (2, 2, 8192)]
+         (1, 65, 1023), (1, 11, 1024), (2, 3, 1032), (1, 33, 4096), (1, 9, 5120), (1, 4, 5121), (1, 3, 7168), (2, 2, 8192),
+         (1, 6, 2047), (2, 3, 3001)]
+# enough rows for every slice to take several (the rings go round)
+LONG = [(2, 1500, 200), (1, 3000, 1280), (5, 400, 96), (1, 2500, 1023), (2, 1700, 5120), (1, 1300, 8190)]
 
 
 @pytest.mark.parametrize("kind", ["layer", "rms", "none"])
-@pytest.mark.parametrize("B,N,C", SIZES)
+@pytest.mark.parametrize("B,N,C", SIZES + LONG)
 def test_forward(V, kind, B, N, C):
     for i, (ti, to) in enumerate(PAIRS):
         dti, dto = TYPES[ti], TYPES[to]
@@ -176,7 +179,7 @@ def _backward(dy, x, mean, rstd, kind, w, b, G):
 
 
 @pytest.mark.parametrize("kind", ["layer", "rms", "none"])
-@pytest.mark.parametrize("B,N,C", SIZES + [(2, 1500, 200), (1, 3000, 1280), (5, 400, 96)])
+@pytest.mark.parametrize("B,N,C", SIZES + LONG)
 def test_backward(V, kind, B, N, C):
     for i, (ti, to) in enumerate(PAIRS):
         dti, dto = TYPES[ti], TYPES[to]
