@@ -61,6 +61,7 @@ struct Args {
   float* mean;                     // forward: out or null; backward: in
   float* rstd;
   float* part;                     // backward: [B * slices][2][C] partial P1, P2
+  int32_t* done;                   // backward: null, or norm_grad_kernel's counters to clear
   int32_t B, N, C, kind, slices;
   int32_t stages;                  // rows in the ring: 2 to 4
 };
@@ -551,6 +552,8 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
   const TI* res = has_res ? static_cast<const TI*>(a.res) + s.b * a.rb : nullptr;
   TI* dx = static_cast<TI*>(a.y) + s.b * a.yb;
   if (!kWarp && threadIdx.x < 4 * kMaxWarps) (&red[0][0][0])[threadIdx.x] = 0.f;
+  if (a.done != nullptr && blockIdx.x == 0)
+    for (int32_t i = threadIdx.x; i < (a.C + 31) / 32; i += blockDim.x) a.done[i] = 0;
 
   // rows are fetched one after the other: the next one's addresses
   x += first * a.xn;
@@ -713,6 +716,8 @@ norm_bwd_kernel(const __grid_constant__ Args a) {
 // Parameter gradients from the slices' sums. One CTA per 32 channels and sequence: 16 rows of
 // threads add up the slices (a fixed assignment and order), then
 //   dG = w P1 + b P2, dshift = P2, and the sequence's G P1, G P2 for dw, db.
+// The CTA of these channels that comes last adds those up over the sequences, in their order: which CTA
+// it is changes nothing.
 // ------------------------------------------------------------------------------------
 struct GradArgs {
   const float* part;       // [B * slices][2][C]
@@ -720,8 +725,9 @@ struct GradArgs {
   float gain_off;
   float* dgain;            // null or [B][C]
   float* dshift;           // null or [B][C]
-  float* gp;               // [B][2][C]: G P1, G P2 for norm_weight_grad_kernel, or null
-  float* dw;               // one sequence: [C] or null
+  float* gp;               // [B][2][C]: G P1, G P2 (several sequences, dw or db asked for), or null
+  int32_t* done;           // [C / 32]: sequences whose G P1, G P2 are written (the backward kernel clears it)
+  float* dw;               // null or [C]
   float* db;
   int32_t B, C, slices;
 };
@@ -729,10 +735,12 @@ constexpr int kGradRows = 16;
 
 __global__ void __launch_bounds__(32 * kGradRows) norm_grad_kernel(const __grid_constant__ GradArgs a) {
   __shared__ float s1[kGradRows][32], s2[kGradRows][32];
+  __shared__ int last;
   const int32_t col = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int32_t c = blockIdx.x * 32 + col, b = blockIdx.y;
+  const bool have = c < a.C;
   float p1 = 0.f, p2 = 0.f;
-  if (c < a.C) {
+  if (have) {
     const float* part = a.part + static_cast<int64_t>(b) * a.slices * 2 * a.C + c;
 #pragma unroll 8
     for (int32_t i = r; i < a.slices; i += kGradRows) {
@@ -740,42 +748,53 @@ __global__ void __launch_bounds__(32 * kGradRows) norm_grad_kernel(const __grid_
       p2 += part[static_cast<int64_t>(i) * 2 * a.C + a.C];
     }
   }
-  s1[r][col] = p1;
-  s2[r][col] = p2;
-  __syncthreads();
-  if (r != 0 || c >= a.C) return;
+  // the rows' sums, in row 0
+  const auto rows_sum = [&]() {
+    s1[r][col] = p1;
+    s2[r][col] = p2;
+    __syncthreads();
+    if (r != 0) return;
 #pragma unroll
-  for (int i = 1; i < kGradRows; ++i) {
-    p1 += s1[i][col];
-    p2 += s2[i][col];
+    for (int i = 1; i < kGradRows; ++i) {
+      p1 += s1[i][col];
+      p2 += s2[i][col];
+    }
+  };
+  rows_sum();
+  if (r == 0 && have) {
+    const int64_t o = static_cast<int64_t>(b) * a.C + c;
+    if (a.dgain) {
+      const float w = a.w.p ? load_param(a.w, 0, c) : 1.f;
+      a.dgain[o] = a.b.p ? fmaf(w, p1, load_param(a.b, 0, c) * p2) : w * p1;
+    }
+    if (a.dshift) a.dshift[o] = p2;
+    const float G = a.g.p ? a.gain_off + load_param(a.g, b, c) : 1.f;
+    p1 *= G;
+    p2 *= G;
+    if (a.gp) {
+      a.gp[static_cast<int64_t>(b) * 2 * a.C + c] = p1;
+      a.gp[static_cast<int64_t>(b) * 2 * a.C + a.C + c] = p2;
+      __threadfence();
+    }
   }
-  const int64_t o = static_cast<int64_t>(b) * a.C + c;
-  if (a.dgain) {
-    const float w = a.w.p ? load_param(a.w, 0, c) : 1.f;
-    a.dgain[o] = a.b.p ? fmaf(w, p1, load_param(a.b, 0, c) * p2) : w * p1;
-  }
-  if (a.dshift) a.dshift[o] = p2;
-  const float G = a.g.p ? a.gain_off + load_param(a.g, b, c) : 1.f;
-  if (a.dw) a.dw[c] = G * p1;
-  if (a.db) a.db[c] = G * p2;
   if (a.gp) {
-    a.gp[static_cast<int64_t>(b) * 2 * a.C + c] = G * p1;
-    a.gp[static_cast<int64_t>(b) * 2 * a.C + a.C + c] = G * p2;
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.done + blockIdx.x, 1) == a.B - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    p1 = p2 = 0.f;
+    if (have)
+      for (int32_t i = r; i < a.B; i += kGradRows) {
+        p1 += __ldcg(a.gp + static_cast<int64_t>(i) * 2 * a.C + c);
+        p2 += __ldcg(a.gp + static_cast<int64_t>(i) * 2 * a.C + a.C + c);
+      }
+    rows_sum();
   }
-}
-
-// dw, db: the sequences' G P1, G P2 added up in order.
-__global__ void __launch_bounds__(256) norm_weight_grad_kernel(const float* gp, float* dw, float* db, int32_t B,
-                                                               int32_t C) {
-  const int32_t c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= C) return;
-  float a = 0.f, b = 0.f;
-  for (int32_t i = 0; i < B; ++i) {
-    a += gp[static_cast<int64_t>(i) * 2 * C + c];
-    b += gp[static_cast<int64_t>(i) * 2 * C + C + c];
+  if (r == 0 && have) {
+    if (a.dw) a.dw[c] = p1;
+    if (a.db) a.db[c] = p2;
   }
-  if (dw) dw[c] = a;
-  if (db) db[c] = b;
 }
 
 }  // namespace norm

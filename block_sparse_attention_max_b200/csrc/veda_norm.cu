@@ -249,9 +249,9 @@ veda_status veda_norm_fwd(const veda_rows* x, const veda_rows* residual, const v
 size_t veda_norm_bwd_workspace_bytes(int32_t B, int32_t N, int32_t C) {
   if (B <= 0 || N <= 0 || C <= 0 || C > norm::kMaxCols) return 0;
   // partial sums of every slice (slices_for: fewer than kMaxSms * kMaxPerSmBwd + B in all, and at
-  // most one a row), then one row pair per sequence
+  // most one a row), then one row pair per sequence, then a counter per 32 channels
   const int64_t slices = std::min<int64_t>(static_cast<int64_t>(B) * N, kMaxSms * kMaxPerSmBwd + B);
-  return static_cast<size_t>((slices + B) * 2 * C) * sizeof(float);
+  return static_cast<size_t>((slices + B) * 2 * C + (C + 31) / 32) * sizeof(float);
 }
 
 veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* mean, const float* rstd,
@@ -307,6 +307,9 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     a.part = static_cast<float*>(workspace);
     const Kernel k = pick(s, true, vec, x->dtype, dy->dtype);
     if ((st = slices_for(k, s, bytes, sms, true, B, N, a.slices)) != VEDA_OK) return st;
+    float* const pairs = a.part + static_cast<int64_t>(B) * a.slices * 2 * C;
+    const bool over_sequences = B > 1 && (dweight || dbias);
+    if (over_sequences) a.done = reinterpret_cast<int32_t*>(pairs + static_cast<int64_t>(B) * 2 * C);
     k<<<static_cast<unsigned>(B * a.slices), s.threads, bytes, s0>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "norm_bwd_kernel");
@@ -317,17 +320,13 @@ veda_status veda_norm_bwd(const veda_rows* dy, const veda_rows* x, const float* 
     g.gain_off = a.gain_off;
     g.dgain = dgain; g.dshift = dshift;
     g.B = B; g.C = C; g.slices = a.slices;
-    if (B == 1) {
-      g.dw = dweight; g.db = dbias;
-    } else if (dweight || dbias) {
-      g.gp = a.part + static_cast<int64_t>(B) * a.slices * 2 * C;
+    g.dw = dweight; g.db = dbias;
+    if (over_sequences) {
+      g.gp = pairs;
+      g.done = a.done;
     }
     norm::norm_grad_kernel<<<dim3((C + 31) / 32, B), 32 * norm::kGradRows, 0, s0>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "norm_grad_kernel");
-    if (g.gp) {
-      norm::norm_weight_grad_kernel<<<(C + 255) / 256, 256, 0, s0>>>(g.gp, dweight, dbias, B, C);
-      if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "norm_weight_grad_kernel");
-    }
     return VEDA_OK;
   });
 }
