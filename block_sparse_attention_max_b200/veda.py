@@ -818,9 +818,10 @@ def rotary(x: torch.Tensor, table: RotaryTable, rows: Optional[torch.Tensor] = N
         _separate(out, table.cos_sin, "the table", False)
     if rows is not None:
         _need(rows, torch.int32, "rows", shape=(B, N))
+    cs = table.cos_sin
     _check("veda_rotary", lib().veda_rotary(
-        _ptr(x), _STRIDES3.pack(*x.stride()[:3]), _ptr(out), _STRIDES3.pack(*out.stride()[:3]), _DTYPE[x.dtype],
-        _ptr(table.cos_sin), table.cos_sin.shape[0], _ptr(rows), 2 * table.cos_sin.shape[1], int(table.interleaved),
+        x.data_ptr(), _STRIDES3.pack(*x.stride()[:3]), out.data_ptr(), _STRIDES3.pack(*out.stride()[:3]),
+        _DTYPE[x.dtype], cs.data_ptr(), cs.shape[0], _ptr(rows), 2 * cs.shape[1], int(table.interleaved),
         int(bool(inverse)), B, N, H, D, _stream(stream)))
     return out
 
@@ -898,7 +899,8 @@ def _rows3(t: torch.Tensor, name: str, dtype=None, shape=None, written=False) ->
 def _rows(t: Optional[torch.Tensor]):
     if t is None:
         return None
-    return _ROWS.pack(t.data_ptr(), t.stride(0), t.stride(1), _DTYPE[t.dtype])
+    sb, sn, _ = t.stride()
+    return _ROWS.pack(t.data_ptr(), sb, sn, _DTYPE[t.dtype])
 
 
 def _vectors(B: int, C: int, weight, bias, gain, shift, gain_name: str, offset: float):
@@ -935,6 +937,8 @@ def _norm_kind(kind: str) -> int:
 
 def _norm_fwd(x, x3, residual, params, residual_scale, kind, eps, out_dtype, out, want_stats, stream):
     B, N, C = x3.shape
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"out_dtype: expected bfloat16, float16 or float32, got {out_dtype}")
     if residual is not None:
         residual = _rows3(residual, "residual", out_dtype, x3.shape)
     if out is None:

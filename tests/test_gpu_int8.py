@@ -192,3 +192,25 @@ def test_linear_shapes_streams_graph(V):
         for _ in range(3):
             g.replay()
         assert torch.equal(y, V.int8_linear(x2, w, bias))
+
+
+def test_refuses_types_and_shapes(V):
+    x, w = _rand(4, 64, dtype=torch.bfloat16), V.quantize_int8(_rand(8, 64))
+    with pytest.raises(TypeError, match="float64"):
+        V.quantize_int8(x.double())
+    with pytest.raises(TypeError, match="out_dtype"):
+        V.int8_linear(x, w, out_dtype=torch.float64)
+    with pytest.raises(ValueError, match="rows of 32"):
+        V.int8_linear(x[:, :32], w)
+    with pytest.raises(ValueError, match="a has rows"):
+        V.int8_matmul(V.quantize_int8(x[:, :32]), w)
+    with pytest.raises(ValueError, match="bias: expected shape"):
+        V.int8_linear(x, w, _rand(7))
+    with pytest.raises(TypeError, match="bias"):
+        V.int8_linear(x, w, _rand(8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="rows of one stride"):
+        V.int8_linear(_rand(2, 4, 128, dtype=torch.bfloat16)[:, :3, :64], w)
+    with pytest.raises(ValueError, match="expected 4 rows"):
+        V.quantize_int8(x, out=w)
+    with pytest.raises(ValueError, match="overlap in memory"):
+        V.int8_matmul(V.quantize_int8(x), w, out=_rand(1, 8).expand(4, 8))

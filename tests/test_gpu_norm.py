@@ -302,3 +302,30 @@ def test_many_sequences(V):
     # dweight: B sequences are added up one after the other
     ref, b = sums["weight"]
     assert R.worst(g.dweight, ref, b * (B + 60) / 61, torch.float32) <= 1
+
+
+def test_refuses_types_and_shapes(V):
+    x, res = _rand(2, 3, 64, dtype=torch.bfloat16), _rand(2, 3, 64)
+    with pytest.raises(TypeError, match="float64"):
+        V.norm_modulate(x, out_dtype=torch.float64)
+    with pytest.raises(TypeError, match="float64"):
+        V.norm_gate_add(x, res.double())
+    with pytest.raises(V.VedaError, match="types"):
+        V.norm_modulate(x, out_dtype=torch.float16)
+    with pytest.raises(V.VedaError, match="8192"):
+        V.norm_modulate(_rand(1, 2, 8193))
+    with pytest.raises(ValueError, match="scale: expected shape"):
+        V.norm_modulate(x, _rand(3, 64))
+    with pytest.raises(TypeError, match="one type"):
+        V.norm_modulate(x, _rand(2, 64), _rand(2, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="stats"):
+        V.norm_modulate_bwd(x, x, None)
+    with pytest.raises(ValueError, match="overlaps"):
+        big = _rand(2, 4, 64, dtype=torch.bfloat16)
+        V.norm_modulate(big[:, 1:], out=big[:, :3])
+    with pytest.raises(ValueError, match="overlap in memory"):
+        V.norm_modulate(x, out=_rand(1, 3, 64, dtype=torch.bfloat16).expand(2, 3, 64))
+    with pytest.raises(ValueError, match="residual: expected shape"):
+        V.norm_gate_add(x, res[:1])
+    with pytest.raises(ValueError, match="kind"):
+        V.norm_modulate(x, kind="batch")

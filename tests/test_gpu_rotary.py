@@ -261,3 +261,28 @@ def test_full_clip_rows(V):
     tok = torch.randint(0, w.N, (500,), device=DEV)
     ref, mag = R.rotate(x[:, tok].double(), t.cos_sin[tok].double()[None, :, None], 128, True)
     assert R.worst(y[:, tok], ref, 3 * R.U32 * mag, torch.bfloat16) <= 1.0
+
+
+def test_refuses_types_and_shapes(V):
+    x, t = _rand(2, 6, 3, 64, dtype=torch.bfloat16), _table(V, 6, 64, True)
+    with pytest.raises(TypeError, match="float64"):
+        V.rotary(x.double(), t)
+    with pytest.raises(ValueError, match="dimensions"):
+        V.rotary(x[0], t)
+    with pytest.raises(V.VedaError, match="rot_dim"):
+        V.rotary(x[..., :32].contiguous(), t)                     # a table of more channels than the head
+    with pytest.raises(V.VedaError, match="rows"):
+        V.rotary(x[:, :5], t)
+    with pytest.raises(ValueError, match="rows: expected shape"):
+        V.rotary(x, t, rows=torch.zeros((2, 5), dtype=torch.int32, device=DEV))
+    with pytest.raises(TypeError, match="rows"):
+        V.rotary(x, t, rows=torch.zeros((2, 6), dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError, match="overlaps"):
+        y = _rand(2, 7, 3, 64, dtype=torch.bfloat16)
+        V.rotary(y[:, 1:], t, out=y[:, :6])
+    with pytest.raises(ValueError, match="contiguous"):
+        V.rotary(x.transpose(2, 3), t)
+    with pytest.raises(ValueError, match="cos_sin"):
+        V.rotary(x, V.RotaryTable(t.cos_sin[..., 0], True))
+    with pytest.raises(ValueError, match="current device|CUDA"):
+        V.rotary(x, V.RotaryTable(t.cos_sin.cpu(), True))
