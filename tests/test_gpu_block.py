@@ -109,7 +109,8 @@ def test_attention_block(V, w, xdt):
 def test_training_step_gradients(V):
     """Norm, rotary, sparse attention, gated residual and their backward against automatic
     differentiation in 64 bits over the same block lists. The attention's rule is 2e-2 (max) and 2e-3
-    (mean) of the gradient's scale; the chain rounds to bf16 six more times, 2^-9 each at most."""
+    (mean) of the gradient's scale; the chain rounds to bf16 six more times, by at most 2^-8 each; half of
+    that sum is allowed."""
     w = synth.TINY
     B, N, H = w.B, w.N, w.H
     C = H * 128
