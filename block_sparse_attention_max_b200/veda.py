@@ -629,6 +629,12 @@ _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _KIND = {"layer": 0, "rms": 1, "none": 2}
 
 
+def _fits(name: str, shape: Sequence[int]) -> None:
+    """Sizes the library takes in 32 bits: a larger one would arrive as its remainder."""
+    if max(shape, default=0) > 0x7fffffff:
+        raise ValueError(f"{name}: sizes of 2^31 and more are not supported, got {tuple(shape)}")
+
+
 def _need_strided(t: torch.Tensor, name: str, ndim: int, dtype: Optional[torch.dtype] = None,
                   shape: Optional[Sequence[int]] = None, written: bool = False) -> None:
     """Checks of a tensor whose leading dimensions may have any stride: type, shape, device,
@@ -807,6 +813,7 @@ def rotary(x: torch.Tensor, table: RotaryTable, rows: Optional[torch.Tensor] = N
     """veda_rotary: x [B, N, H, D] (bf16, fp16 or fp32; any strides, channels contiguous) turned by
     the table's row of each token -- row n, row b N + n (a table of B N rows), or rows[b, n]
     (int32). ``inverse`` is the transpose, which the gradient takes. ``out`` may be x."""
+    _fits("x", x.shape)
     _need_strided(x, "x", 4)
     B, N, H, D = x.shape
     table._check()
@@ -892,6 +899,8 @@ class NormGrads:
 def _rows3(t: torch.Tensor, name: str, dtype=None, shape=None, written=False) -> torch.Tensor:
     """[N, C] as [1, N, C], checked."""
     t = t.unsqueeze(0) if t.dim() == 2 else t
+    if shape is None:
+        _fits(name, t.shape)
     _need_strided(t, name, 3, dtype, shape, written)
     return t
 
@@ -1101,6 +1110,7 @@ def quantize_int8(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) 
     """veda_quantize_int8: rows of x [..., K] (bf16, fp16 or fp32) to codes with a scale for each
     row -- tokens of an activation, output channels of a weight [N, K]."""
     m = _matrix(x, "x")
+    _fits("x", m.shape)
     _need_strided(m, "x", 2)
     rows, K = m.shape
     if out is None:
@@ -1121,6 +1131,8 @@ def int8_matmul(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
     """veda_int8_matmul: y[m, n] = (a[m] . w[n]) a.scale[m] w.scale[n] + bias[n] (bias fp32 [N]);
     y [M, N] in bf16, fp16 or fp32."""
+    _fits("a", a.codes.shape)
+    _fits("w", w.codes.shape)
     a._check("a")
     w._check("w")
     if a.K != w.K:
@@ -1148,6 +1160,8 @@ def int8_linear(x: torch.Tensor, w: Int8Rows, bias: Optional[torch.Tensor] = Non
     """veda_int8_linear: x [..., K] W^T + bias in 8-bit integers -- ``quantize_int8`` of x's rows and
     ``int8_matmul`` with the weight's rows in one call; [..., N] in x's type (or out_dtype)."""
     m = _matrix(x, "x")
+    _fits("x", m.shape)
+    _fits("w", w.codes.shape)
     _need_strided(m, "x", 2)
     w._check("w")
     M, K = m.shape

@@ -214,3 +214,22 @@ def test_positions():
     assert p.shape == (3, 26) and p.dtype == np.int32
     for n, thw in ((0, (0, 0, 0)), (5, (0, 1, 1)), (12, (1, 0, 0)), (23, (1, 2, 3)), (24, (4, 4, 4)), (25, (5, 5, 5))):
         assert tuple(p[:, n]) == thw
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that the library takes in 32 bits must not wrap: 2^32 + 5 rows would pass as 5."""
+    many = 2 ** 32 + 5
+    cs = veda.RotaryTable(torch.ones(1, 1, 2), True)
+    wide = torch.zeros(1, 16).expand(many, 16)
+    w = veda.Int8Rows(torch.zeros(1, 16, dtype=torch.int8), torch.ones(1), 16)
+    for call in (lambda: veda.rotary(torch.zeros(1, 1, 1, 2).expand(1, many, 1, 2), cs),
+                 lambda: veda.norm_modulate(wide),
+                 lambda: veda.norm_gate_add(wide, wide),
+                 lambda: veda.norm_modulate_bwd(wide, wide, None, kind="none"),
+                 lambda: veda.norm_gate_add_bwd(wide, wide, None, kind="none"),
+                 lambda: veda.int8_linear(wide, w),
+                 lambda: veda.quantize_int8(wide), lambda: veda.quantize_int8(wide.t()),
+                 lambda: veda.int8_matmul(veda.Int8Rows(torch.zeros(1, 16, dtype=torch.int8).expand(many, 16),
+                                                        torch.ones(1).expand(many), 16), w)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
