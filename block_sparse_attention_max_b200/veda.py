@@ -715,8 +715,11 @@ def rotary_frequencies(dims, theta: float = 10000.0, scaling: str = "none", fact
     theta * factor^(d / (d - 2)), which keeps the fastest pair and slows the slowest by the factor;
     ``yarn`` (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models")
     keeps the pairs that turn more than beta_fast times within original_length, divides those that
-    turn less than beta_slow times by the factor, goes linearly in the pair index between, and
-    scales the turned vectors by 0.1 ln(factor) + 1.
+    turn less than beta_slow times by the factor, and scales the turned vectors by
+    0.1 ln(factor) + 1. Between the two it goes linearly in the pair index (the paper's formula is
+    linear in the number of turns), from the last whole pair before the one that turns beta_fast
+    times to the first whole pair behind the one that turns beta_slow times; either may lie outside
+    the head, and the ramp is then cut off there, not bent.
     """
     dims = [int(dims)] if isinstance(dims, (int, np.integer)) else [int(d) for d in dims]
     if not dims or any(d < 0 or d % 2 for d in dims) or sum(dims) == 0:
@@ -742,8 +745,8 @@ def rotary_frequencies(dims, theta: float = 10000.0, scaling: str = "none", fact
             f = f / factor
         elif scaling == "yarn":
             pair = lambda turns: d * np.log(original_length / (2 * np.pi * turns)) / (2 * np.log(theta))
-            low, high = max(np.floor(pair(beta_fast)), 0.0), min(np.ceil(pair(beta_slow)), d / 2 - 1.0)
-            ramp = np.clip((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+            low, high = np.floor(pair(beta_fast)), np.ceil(pair(beta_slow))
+            ramp = np.clip((i - low) / max(high - low, 1.0), 0.0, 1.0)
             f = f * (1.0 - ramp) + f / factor * ramp
             amplitude = 0.1 * float(np.log(factor)) + 1.0
         inv.append(f)

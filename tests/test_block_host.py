@@ -233,3 +233,27 @@ def test_sizes_past_32_bits_are_refused():
                                                         torch.ones(1).expand(many), 16), w)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+@pytest.mark.parametrize("d,theta,length", [(128, 1e4, 4096), (128, 1e4, 1 << 20), (64, 1e4, 131072), (44, 256.0, 8192),
+                                            (128, 1e4, 54000), (128, 1e4, 1 << 17), (8, 1e4, 100), (128, 1e4, 64)])
+@pytest.mark.parametrize("fast,slow,factor", [(32.0, 1.0, 4.0), (8.0, 2.0, 16.0)])
+def test_yarn_ramp(d, theta, length, fast, slow, factor):
+    """Every pair against the ramp: linear in the pair index between the whole pairs around those that
+    turn beta_fast and beta_slow times within the length, also where one of them lies outside the head
+    (the slowest pair turns 1 to 32 times; the fastest fewer than 32)."""
+    f = veda.rotary_frequencies(d, theta, "yarn", factor, length, fast, slow)
+    base = veda.rotary_frequencies(d, theta).inv_freq
+    # the pair index, a real number, whose frequency turns t times within the length
+    index = lambda t: math.log(length / (2 * math.pi * t)) * d / (2 * math.log(theta))
+    low, high = math.floor(index(fast)), math.ceil(index(slow))
+    for i in range(d // 2):
+        ramp = min(max((i - low) / (high - low), 0.0), 1.0)
+        assert math.isclose(f.inv_freq[i], base[i] * (1 - ramp + ramp / factor), rel_tol=1e-12), i
+        turns = length * base[i] / (2 * math.pi)
+        if turns < slow and i >= high:
+            assert math.isclose(f.inv_freq[i], base[i] / factor, rel_tol=1e-12)
+        if i <= low:
+            assert f.inv_freq[i] == base[i] and turns > fast * (1 - 1e-12)
+        if turns > slow * (1 + 1e-12):                     # only slower pairs get the whole factor
+            assert f.inv_freq[i] > base[i] / factor
