@@ -1323,7 +1323,9 @@ class HostPipeline:
     at once). Device copies of the raster inputs and of the raster output are kept per slot
     (``depth`` slots); CUDA events order every reuse of a slot after the work that last read
     it, so a clip's result does not depend on its neighbours. ``rotary``: positions for Q and K of
-    every clip. ``synchronize`` waits for every submitted clip's output to be in its host tensor.
+    every clip. What the current stream holds when the pipeline is made (the table's kernel, the
+    maps) comes before the first clip. ``synchronize`` waits for every submitted clip's output to be in
+    its host tensor.
     """
 
     def __init__(self, B: int, N: int, H: int, maps: DeviceMaps, rho: Sequence[Tuple[int, int]],
@@ -1340,6 +1342,10 @@ class HostPipeline:
         self.outputs = [torch.empty((B, N, H, 128), **bf) for _ in range(depth)]
         self.bufs = PathBuffers.allocate(B, N, H, maps, rho, device)
         self.h2d, self.comp, self.d2h = (torch.cuda.Stream(device) for _ in range(3))
+        # the buffers' memory, the lists' zeros, the maps and the table are the current stream's (d2h
+        # follows comp)
+        for st in (self.h2d, self.comp):
+            st.wait_stream(torch.cuda.current_stream(device))
         ev = lambda: [torch.cuda.Event() for _ in range(depth)]
         self.in_ready, self.in_free, self.out_ready, self.out_free = ev(), ev(), ev(), ev()
         self.n = 0

@@ -257,3 +257,29 @@ def test_yarn_ramp(d, theta, length, fast, slow, factor):
             assert f.inv_freq[i] == base[i] and turns > fast * (1 - 1e-12)
         if turns > slow * (1 + 1e-12):                     # only slower pairs get the whole factor
             assert f.inv_freq[i] > base[i] / factor
+
+
+class _FakeStream:
+    made: list = []
+
+    def __init__(self, device=None):
+        self.after = []                                     # streams whose work so far comes before this one's
+        _FakeStream.made.append(self)
+
+    def wait_stream(self, s):
+        self.after.append(s)
+
+
+def test_host_pipeline_waits_for_the_stream_it_is_made_on(L, monkeypatch):
+    """The table, the tile maps and the buffers come from the stream that is current when the pipeline is
+    made: the pipeline's own streams must not read or write them before that stream's work has run."""
+    monkeypatch.setattr(_FakeStream, "made", [])
+    current = _FakeStream()
+    monkeypatch.setattr(torch.cuda, "Stream", _FakeStream)
+    monkeypatch.setattr(torch.cuda, "Event", lambda *a, **k: object())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    maps = veda.build_tile_map((2, 8, 16), [(1, 8, 16)]).to("cpu")
+    table = veda.RotaryTable(torch.ones(256, 64, 2), True)
+    pipe = veda.HostPipeline(1, 256, 1, maps, [(1, 10)], 0.1, "cpu", rotary=table)
+    for s in (pipe.h2d, pipe.comp):
+        assert s.after == [current]

@@ -203,6 +203,33 @@ def test_host_pipeline_with_positions(V):
         assert torch.equal(o, ref.o.cpu())
 
 
+def test_host_pipeline_made_behind_queued_work(V):
+    """A table that the current stream has still to make when the pipeline is built and the first clips
+    are submitted: about 0.1 s of copies are queued ahead of it."""
+    w = synth.SMALL
+    maps, table = _setup(V, w)
+    scale = 1 / math.sqrt(128)
+    pin = lambda t: t.cpu().pin_memory()
+    clip = [pin(_rand(w.B, w.N, w.H, 128, seed=j, dtype=torch.bfloat16)) for j in range(3)]
+    clip += [pin(_rand(w.H, 128, 384, seed=j, scale=0.02)) for j in (4, 5)]
+    ref = V.sparse_attention(*[t.to(DEV) for t in clip], maps, w.rho, scale, rotary=table).o.cpu()
+    outs = [torch.empty((w.B, w.N, w.H, 128), dtype=torch.bfloat16).pin_memory() for _ in range(3)]
+    f = V.rotary_frequencies((44, 42, 42))
+    pos = torch.from_numpy(V.rotary_positions(w.grid, w.n_tail)).to(DEV)
+    cs = torch.zeros_like(table.cos_sin)
+    a, b = torch.zeros(1 << 30, device=DEV, dtype=torch.uint8), torch.zeros(1 << 30, device=DEV, dtype=torch.uint8)
+    torch.cuda.synchronize()
+    for _ in range(300):
+        b.copy_(a)
+    late = V.rotary_table(pos, f.inv_freq, f.axis, out=cs)
+    pipe = V.HostPipeline(w.B, w.N, w.H, maps, w.rho, scale, DEV, rotary=late)
+    for o in outs:
+        pipe.submit(*clip, o)
+    pipe.synchronize()
+    for o in outs:
+        assert torch.equal(o, ref)
+
+
 def test_two_threads_on_their_own_streams(V):
     """Calls enqueued from two host threads at once, each on its stream: bit for bit the results of
     calls one after the other."""
