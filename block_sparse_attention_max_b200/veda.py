@@ -1218,7 +1218,17 @@ class PathBuffers:
     o: torch.Tensor
 
     @staticmethod
-    def allocate(B: int, N: int, H: int, maps: DeviceMaps, rho, device) -> "PathBuffers":
+    def allocate(B: int, N: int, H: int, maps: DeviceMaps, rho, device, stream=None) -> "PathBuffers":
+        """Buffers for work on ``stream`` (None: the current one): its memory, and the lists' zeros in
+        its order; kept from reuse until what the current stream does with them later has run."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                bufs = PathBuffers.allocate(B, N, H, maps, rho, device)
+            ls = bufs.lists
+            for t in (bufs.q_t, bufs.k_t, bufs.v_t, bufs.pooled_q, bufs.pooled_k, bufs.scores, bufs.workspace, bufs.o_t,
+                      bufs.lse, bufs.o, ls.full_cnt, ls.full_idx, ls.part_cnt, ls.part_idx):
+                t.record_stream(torch.cuda.current_stream())
+            return bufs
         nT, Npad, D = maps.nT, maps.Npad, 128
         bf = dict(dtype=torch.bfloat16, device=device)
         f32 = dict(dtype=torch.float32, device=device)
@@ -1249,7 +1259,7 @@ def sparse_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: torc
     way into the tiles (``rotary_permute_pool``).
     """
     B, N, H, D = q.shape
-    bufs = buffers or PathBuffers.allocate(B, N, H, maps, rho, q.device)
+    bufs = buffers or PathBuffers.allocate(B, N, H, maps, rho, q.device, stream)
     if rotary is None:
         permute_pool(q, maps, bufs.q_t, bufs.pooled_q, stream)
         permute_pool(k, maps, bufs.k_t, bufs.pooled_k, stream)
@@ -1307,9 +1317,6 @@ def attention_block(x: torch.Tensor, w: BlockWeights, scale: Optional[torch.Tens
     a8 = quantize_int8(a, stream=stream)
     q, k, v = (int8_matmul(a8, r, b, stream=stream).view(B, N, H, 128)
                for r, b in ((w.q, w.q_bias), (w.k, w.k_bias), (w.v, w.v_bias)))
-    if buffers is None and stream is not None:
-        with torch.cuda.stream(stream):
-            buffers = PathBuffers.allocate(B, N, H, maps, rho, x.device)
     bufs = sparse_attention(q, k, v, w.pred_q, w.pred_k, maps, rho, softmax_scale, buffers, stream, rotary=table)
     o = int8_linear(bufs.o.view(B, N, H * 128), w.o, w.o_bias, stream=stream)
     return norm_gate_add(o, x, gate, w.post_weight, None, w.post_kind, w.eps, residual_scale, stream=stream)

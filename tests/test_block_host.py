@@ -283,3 +283,30 @@ def test_host_pipeline_waits_for_the_stream_it_is_made_on(L, monkeypatch):
     pipe = veda.HostPipeline(1, 256, 1, maps, [(1, 10)], 0.1, "cpu", rotary=table)
     for s in (pipe.h2d, pipe.comp):
         assert s.after == [current]
+
+
+def test_path_buffers_come_from_the_launching_stream(L, monkeypatch):
+    """sparse_attention(stream=s) without buffers: memory and the lists' zeros on s, not on the current
+    stream, and every buffer kept from reuse while the current stream still reads it."""
+    import contextlib
+    current, other, kept, active = _FakeStream(), _FakeStream(), [], []
+
+    @contextlib.contextmanager
+    def on(s):
+        active.append(s)
+        yield
+        active.pop()
+    made = []
+    real = torch.empty, torch.zeros
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: active[-1] if active else current)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append((real[0](*a, **k), active[-1:])) or made[-1][0])
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: made.append((real[1](*a, **k), active[-1:])) or made[-1][0])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((t, s)))
+    monkeypatch.setattr(veda, "permute_pool", lambda *a, **k: (_ for _ in ()).throw(StopIteration))
+    maps = veda.build_tile_map((2, 8, 16), [(1, 8, 16)]).to("cpu")
+    q = real[1]((1, 256, 1, 128), dtype=torch.bfloat16)
+    with pytest.raises((StopIteration, RuntimeError)):
+        veda.sparse_attention(q, q, q, None, None, maps, [(1, 10)], 0.1, stream=other)
+    assert len(made) == 14 and all(s == [other] for _, s in made)
+    assert {id(t) for t, _ in made} == {id(t) for t, s in kept if s is current}
