@@ -664,23 +664,37 @@ def _need_strided(t: torch.Tensor, name: str, ndim: int, dtype: Optional[torch.d
             extent = st * (n - 1) + extent
 
 
-def _separate(out: torch.Tensor, t: Optional[torch.Tensor], name: str, same_ok: bool) -> None:
+def _separate(out: torch.Tensor, t: Optional[torch.Tensor], name: str, same_ok: bool, what: str = "out") -> None:
     """out may be t itself (where same_ok), else they must not share memory."""
     if t is None or out.numel() == 0 or t.numel() == 0:
         return
-    if out.data_ptr() == t.data_ptr() and out.stride() == t.stride() and out.shape == t.shape and out.dtype == t.dtype:
+    if (out.data_ptr() == t.data_ptr() and out.shape == t.shape and out.dtype == t.dtype
+            and all(a == b for a, b, n in zip(out.stride(), t.stride(), out.shape) if n > 1)):
         if same_ok:
             return
-        raise ValueError(f"out must not be {name}")
+        raise ValueError(f"{what} must not be {name}")
     a, b = _span(out), _span(t)
-    if a[0] < b[1] and b[0] < a[1]:
-        raise ValueError(f"out overlaps {name} in memory")
+    if a[0] < b[1] and b[0] < a[1] and not _apart(out, t):
+        raise ValueError(f"{what} overlaps {name} in memory")
 
 
 def _span(t: torch.Tensor) -> Tuple[int, int]:
     """First byte and one past the last byte of a tensor's elements."""
     n = t.numel() if t.is_contiguous() else 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     return t.data_ptr(), t.data_ptr() + t.element_size() * n
+
+
+def _apart(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors are seen to share no byte although their spans meet, as slices of one buffer
+    do: for some stride S of either, dimensions whose stride is a multiple of S leave an address's
+    remainder by S alone, and the others' extents are two separate pieces of the circle of remainders."""
+    dims = [[(n, st * t.element_size()) for n, st in zip(t.shape, t.stride()) if n > 1] for t in (a, b)]
+    for S in {st for d in dims for _, st in d if st > 0}:
+        ea, eb = (t.element_size() + sum((n - 1) * st for n, st in d if st % S) for t, d in zip((a, b), dims))
+        gap = (b.data_ptr() - a.data_ptr()) % S
+        if gap >= ea and gap + eb <= S:
+            return True
+    return False
 
 
 def _new(like: torch.Tensor, shape, dtype: torch.dtype, stream) -> torch.Tensor:

@@ -310,3 +310,57 @@ def test_path_buffers_come_from_the_launching_stream(L, monkeypatch):
         veda.sparse_attention(q, q, q, None, None, maps, [(1, 10)], 0.1, stream=other)
     assert len(made) == 14 and all(s == [other] for _, s in made)
     assert {id(t) for t, _ in made} == {id(t) for t, s in kept if s is current}
+
+
+def _bytes_of(t):
+    idx = np.zeros(tuple(t.shape), np.int64)
+    for d, (n, st) in enumerate(zip(t.shape, t.stride())):
+        idx += (np.arange(n) * st).reshape([-1 if i == d else 1 for i in range(t.dim())])
+    first = (t.data_ptr() + idx.reshape(-1) * t.element_size())[:, None]
+    return set((first + np.arange(t.element_size())).reshape(-1).tolist())
+
+
+def _refused(out, t, same_ok=True):
+    try:
+        veda._separate(out, t, "x", same_ok)
+        return False
+    except ValueError:
+        return True
+
+
+def test_slices_of_one_buffer_do_not_overlap():
+    big, even = torch.zeros(3, 5, 40), torch.zeros(3, 6, 40)
+    a, b = big[..., :16], big[..., 16:32]
+    for x, y in ((a, b), (b, a), (a, big[..., 24:]), (even[:, ::2], even[:, 1::2]), (big[:2], big[2:]),
+                 (big[:, :2, :16], big[:, 3:, :16]), (big.view(3, 5, 4, 10)[:, :, :2], big.view(3, 5, 4, 10)[:, :, 2:]),
+                 (a, big.view(torch.float16)[..., 32:64]), (a[0], b[0])):
+        assert not _refused(x, y)
+    for x, y in ((a, big[..., 15:31]), (big[..., 15:31], a), (big[:, :3], big[:, 2:]), (a, big), (a, big[..., 1:17]),
+                 (big[..., ::2], big[..., 1:]), (a, big.view(torch.float16)[..., 31:63]), (a, big[1:2, 1:2, 3:4])):
+        assert _refused(x, y)
+    # one place for both is an in-place call, whatever the strides of dimensions of one element are
+    assert not _refused(a, big[..., :16]) and _refused(a, big[..., :16], same_ok=False)
+    one = big[1:2]
+    assert not _refused(one, one.as_strided((1, 5, 40), (7, 40, 1)))
+
+
+def test_overlap_check_against_the_bytes():
+    """Random strided views of one buffer: two that share a byte are never let through."""
+    rng = np.random.default_rng(3)
+    base = torch.zeros(4096, dtype=torch.uint8)
+    accepted = 0
+    for _ in range(4000):
+        views = []
+        for _ in range(2):
+            dt = [torch.uint8, torch.float16, torch.float32][rng.integers(3)]
+            t = base.view(dt)
+            shape = rng.integers(1, 5, 3).tolist()
+            inner = int(rng.choice([1, 1, 2]))
+            s1 = shape[2] * inner + int(rng.integers(0, 9))
+            s0 = s1 * shape[1] + int(rng.integers(0, 9))
+            views.append(t.as_strided(shape, (s0, s1, inner), int(rng.integers(0, 60))))
+        same = views[0].data_ptr() == views[1].data_ptr() and views[0].dtype == views[1].dtype
+        if not _refused(*views, same_ok=False):
+            accepted += 1
+            assert same is False and not (_bytes_of(views[0]) & _bytes_of(views[1]))
+    assert accepted > 500

@@ -124,6 +124,25 @@ def test_strided_rows_and_slices(V):
     assert torch.equal(V.norm_modulate(flat, sc[0], sh[0]), y[0])             # [N, C] with [C] vectors
 
 
+@pytest.mark.parametrize("C", [64, 1016, 1023, 2048])
+def test_two_slices_of_one_buffer(V, C):
+    """Block output and stream side by side in the rows of one buffer, the result in the stream's place
+    and in a third slice: nothing else changes."""
+    B, N = 2, 37
+    big = _rand(B, N, 3 * C, seed=60, dtype=torch.bfloat16)
+    gate, dy = _rand(B, C, seed=61), _rand(B, N, C, seed=62, dtype=torch.bfloat16)
+    keep = big.clone()
+    res, o, other = big[..., :C], big[..., C:2 * C], big[..., 2 * C:]
+    want, st = V.norm_gate_add(o.contiguous(), res.contiguous(), gate, want_stats=True)
+    assert torch.equal(V.norm_gate_add(o, res, gate, out=other), want)
+    assert torch.equal(big[..., :2 * C], keep[..., :2 * C])
+    V.norm_gate_add(o, res, gate, out=res)
+    assert torch.equal(res, want) and torch.equal(o, keep[..., C:2 * C]) and torch.equal(other, want)
+    ref = V.norm_gate_add_bwd(dy, o.contiguous(), st, gate)
+    got = V.norm_gate_add_bwd(dy, o, st, gate, out=other)
+    assert torch.equal(got.dx, ref.dx) and torch.equal(big[..., :C], want) and torch.equal(o, keep[..., C:2 * C])
+
+
 def test_in_place_and_empty(V):
     x = _rand(2, 30, 640, seed=5, dtype=torch.bfloat16)
     ref = V.norm_modulate(x)
