@@ -678,6 +678,12 @@ def _separate(out: torch.Tensor, t: Optional[torch.Tensor], name: str, same_ok: 
         raise ValueError(f"{what} overlaps {name} in memory")
 
 
+def _separate_all(out: torch.Tensor, what: str, *others: Tuple[Optional[torch.Tensor], str]) -> None:
+    """A written buffer against the named others (None: not there)."""
+    for t, name in others:
+        _separate(out, t, name, False, what)
+
+
 def _span(t: torch.Tensor) -> Tuple[int, int]:
     """First byte and one past the last byte of a tensor's elements."""
     n = t.numel() if t.is_contiguous() else 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
@@ -818,7 +824,9 @@ def rotary_table(positions: torch.Tensor, inv_freq: np.ndarray, axis: Optional[n
     axes, rows = positions.shape
     if out is None:
         out = _new(positions, (rows, len(inv), 2), torch.float32, stream)
-    _need(out, torch.float32, "out", shape=(rows, len(inv), 2))
+    else:
+        _need(out, torch.float32, "out", shape=(rows, len(inv), 2))
+        _separate(out, positions, "positions", False)
     _check("veda_rotary_table", lib().veda_rotary_table(
         _ptr(positions), axes, rows, inv.ctypes.data, ax.ctypes.data, len(inv), float(amplitude), _ptr(out),
         _stream(stream)))
@@ -834,14 +842,14 @@ def rotary(x: torch.Tensor, table: RotaryTable, rows: Optional[torch.Tensor] = N
     _need_strided(x, "x", 4)
     B, N, H, D = x.shape
     table._check()
+    if rows is not None:
+        _need(rows, torch.int32, "rows", shape=(B, N))
     if out is None:
         out = _new(x, (B, N, H, D), x.dtype, stream)
     else:
         _need_strided(out, "out", 4, x.dtype, x.shape, written=True)
         _separate(out, x, "x", True)
-        _separate(out, table.cos_sin, "the table", False)
-    if rows is not None:
-        _need(rows, torch.int32, "rows", shape=(B, N))
+        _separate_all(out, "out", (table.cos_sin, "the table"), (rows, "rows"))
     cs = table.cos_sin
     _check("veda_rotary", lib().veda_rotary(
         x.data_ptr(), _STRIDES3.pack(*x.stride()[:3]), out.data_ptr(), _STRIDES3.pack(*out.stride()[:3]),
@@ -860,13 +868,17 @@ def rotary_permute_pool(x: torch.Tensor, table: RotaryTable, maps: DeviceMaps, o
     B, N, H, D = x.shape
     _need_maps(maps, H, maps.Npad)
     table._check()
+    read = ((x, "x"), (table.cos_sin, "the table"), (maps.tile_map, "the tile map"), (maps.tile_valid, "tile_valid"))
     if out is None:
         out = _new(x, (B, H, maps.Npad, D), torch.bfloat16, stream)
+    else:
+        _need(out, torch.bfloat16, "out", shape=(B, H, maps.Npad, D))
+        _separate_all(out, "out", *read)
     if pooled is None:
         pooled = _new(x, (B, H, maps.Npad // 128, 3, D), torch.float32, stream)
-    _need(out, torch.bfloat16, "out", shape=(B, H, maps.Npad, D))
-    _need(pooled, torch.float32, "pooled", shape=(B, H, maps.Npad // 128, 3, D))
-    _separate(out, x, "x", False)
+    else:
+        _need(pooled, torch.float32, "pooled", shape=(B, H, maps.Npad // 128, 3, D))
+        _separate_all(pooled, "pooled", *read, (out, "out"))
     _check("veda_rotary_permute_pool", lib().veda_rotary_permute_pool(
         _ptr(x), _ptr(out), _ptr(table.cos_sin), table.rows, table.rot_dim, int(table.interleaved),
         _ptr(maps.tile_map), _ptr(maps.tile_valid), _ptr(pooled), B, N, H, D, maps.Npad, _stream(stream)))
@@ -885,8 +897,9 @@ def rotary_unpermute(x_t: torch.Tensor, table: RotaryTable, maps: DeviceMaps, N:
     table._check()
     if out is None:
         out = _new(x_t, (B, N, H, D), torch.bfloat16, stream)
-    _need(out, torch.bfloat16, "out", shape=(B, N, H, D))
-    _separate(out, x_t, "x_t", False)
+    else:
+        _need(out, torch.bfloat16, "out", shape=(B, N, H, D))
+        _separate_all(out, "out", (x_t, "x_t"), (table.cos_sin, "the table"), (maps.tile_map, "the tile map"))
     _check("veda_rotary_unpermute", lib().veda_rotary_unpermute(
         _ptr(x_t), _ptr(out), _ptr(table.cos_sin), table.rows, table.rot_dim, int(table.interleaved),
         int(bool(inverse)), _ptr(maps.tile_map), B, N, H, D, Npad, _stream(stream)))
@@ -961,7 +974,8 @@ def _norm_kind(kind: str) -> int:
     return _KIND[kind]
 
 
-def _norm_fwd(x, x3, residual, params, residual_scale, kind, eps, out_dtype, out, want_stats, stream):
+def _norm_fwd(x, x3, residual, params, read, residual_scale, kind, eps, out_dtype, out, want_stats, stream):
+    """``read``: the parameters and their names, which out must not overlap."""
     B, N, C = x3.shape
     if out_dtype not in _DTYPE:
         raise TypeError(f"out_dtype: expected bfloat16, float16 or float32, got {out_dtype}")
@@ -974,6 +988,7 @@ def _norm_fwd(x, x3, residual, params, residual_scale, kind, eps, out_dtype, out
         out3 = _rows3(out, "out", out_dtype, x3.shape, written=True)
         _separate(out3, x3, "x", True)
         _separate(out3, residual, "the residual", True)
+        _separate_all(out3, "out", *read)
     stats = mean = rstd = None
     if want_stats:
         stats = NormStats(_new(x, (B, N), torch.float32, stream), _new(x, (B, N), torch.float32, stream))
@@ -997,7 +1012,8 @@ def norm_modulate(x: torch.Tensor, scale: Optional[torch.Tensor] = None, shift: 
     x3 = _rows3(x, "x")
     p = _vectors(x3.shape[0], x3.shape[2], weight, bias, scale, shift, "scale", 1.0)
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else x.dtype
-    return _norm_fwd(x, x3, None, p, 0.0, kind, eps, dt, out, want_stats, stream)
+    read = ((weight, "weight"), (bias, "bias"), (scale, "scale"), (shift, "shift"))
+    return _norm_fwd(x, x3, None, p, read, 0.0, kind, eps, dt, out, want_stats, stream)
 
 
 def norm_gate_add(o: torch.Tensor, residual: torch.Tensor, gate: Optional[torch.Tensor] = None,
@@ -1012,10 +1028,12 @@ def norm_gate_add(o: torch.Tensor, residual: torch.Tensor, gate: Optional[torch.
     itself. ``out`` may be the residual (in place)."""
     o3 = _rows3(o, "o")
     p = _vectors(o3.shape[0], o3.shape[2], weight, bias, gate, None, "gate", 0.0)
-    return _norm_fwd(o, o3, residual, p, residual_scale, kind, eps, residual.dtype, out, want_stats, stream)
+    read = ((weight, "weight"), (bias, "bias"), (gate, "gate"))
+    return _norm_fwd(o, o3, residual, p, read, residual_scale, kind, eps, residual.dtype, out, want_stats, stream)
 
 
-def _norm_bwd(dy, x, x3, stats, params, has, residual_grad, residual_scale, kind, out, stream):
+def _norm_bwd(dy, x, x3, stats, params, read, want_dshift, residual_grad, residual_scale, kind, out, stream):
+    """``read``: weight, bias and gain with their names; which of them is given says which gradients are wanted."""
     B, N, C = x3.shape
     dy3 = _rows3(dy, "dy", None, x3.shape)
     res3 = None if residual_grad is None else _rows3(residual_grad, "residual_grad", x.dtype, x3.shape)
@@ -1034,12 +1052,15 @@ def _norm_bwd(dy, x, x3, stats, params, has, residual_grad, residual_scale, kind
         out3 = _rows3(out, "out", x.dtype, x3.shape, written=True)
         for t, n in ((x3, "x"), (dy3, "dy"), (res3, "residual_grad")):
             _separate(out3, t, n, True)
-    gain, shift, weight, bias = has
+        _separate_all(out3, "out", *read)
+        if stats is not None:
+            _separate_all(out3, "out", (stats.mean, "stats.mean"), (stats.rstd, "stats.rstd"))
     f32 = torch.float32
-    dgain = _new(x, (B, C), f32, stream) if gain else None
-    dshift = _new(x, (B, C), f32, stream) if shift else None
-    dweight = _new(x, (C,), f32, stream) if weight else None
-    dbias = _new(x, (C,), f32, stream) if bias else None
+    (weight, _), (bias, _), (gain, _) = read
+    dgain = _new(x, (B, C), f32, stream) if gain is not None else None
+    dshift = _new(x, (B, C), f32, stream) if want_dshift else None
+    dweight = _new(x, (C,), f32, stream) if weight is not None else None
+    dbias = _new(x, (C,), f32, stream) if bias is not None else None
     nbytes = lib().veda_norm_bwd_workspace_bytes(B, N, C)
     work = _new(x, (max(nbytes, 16),), torch.uint8, stream)
     _check("veda_norm_bwd", lib().veda_norm_bwd(
@@ -1059,8 +1080,8 @@ def norm_modulate_bwd(dy: torch.Tensor, x: torch.Tensor, stats: Optional[NormSta
     residual_scale times it added, which saves the separate sum."""
     x3 = _rows3(x, "x")
     p = _vectors(x3.shape[0], x3.shape[2], weight, bias, scale, None, "scale", 1.0)
-    has = (scale is not None, bool(want_dshift), weight is not None, bias is not None)
-    dx, dg, dt, dw, db = _norm_bwd(dy, x, x3, stats, p, has, residual_grad, residual_scale, kind, out, stream)
+    read = ((weight, "weight"), (bias, "bias"), (scale, "scale"))
+    dx, dg, dt, dw, db = _norm_bwd(dy, x, x3, stats, p, read, bool(want_dshift), residual_grad, residual_scale, kind, out, stream)
     return NormGrads(dx, dw, db, dscale=dg, dshift=dt)
 
 
@@ -1073,8 +1094,8 @@ def norm_gate_add_bwd(dh: torch.Tensor, o: torch.Tensor, stats: Optional[NormSta
     the same block adds on its way (residual_grad=dh)."""
     o3 = _rows3(o, "o")
     p = _vectors(o3.shape[0], o3.shape[2], weight, bias, gate, None, "gate", 0.0)
-    has = (gate is not None, False, weight is not None, bias is not None)
-    dx, dg, _, dw, db = _norm_bwd(dh, o, o3, stats, p, has, None, 0.0, kind, out, stream)
+    read = ((weight, "weight"), (bias, "bias"), (gate, "gate"))
+    dx, dg, _, dw, db = _norm_bwd(dh, o, o3, stats, p, read, False, None, 0.0, kind, out, stream)
     return NormGrads(dx, dw, db, dgate=dg)
 
 
@@ -1137,7 +1158,8 @@ def quantize_int8(x: torch.Tensor, out: Optional[Int8Rows] = None, stream=None) 
         if out.K != K or out.rows != rows:
             raise ValueError(f"out: expected {rows} rows of {K} codes")
         out._check("out")
-        _separate(out.codes, m, "x", False)
+        _separate_all(out.codes, "out.codes", (m, "x"), (out.scale, "out.scale"))
+        _separate_all(out.scale, "out.scale", (m, "x"))
     _check("veda_quantize_int8", lib().veda_quantize_int8(
         _ptr(m), m.stride(0), _DTYPE[m.dtype], _ptr(out.codes), _ptr(out.scale), rows, K, _stream(stream)))
     return out
@@ -1163,9 +1185,8 @@ def int8_matmul(a: Int8Rows, w: Int8Rows, bias: Optional[torch.Tensor] = None,
         out = _new(a.codes, (M, N), out_dtype, stream)
     else:
         _need_strided(out, "out", 2, None, (M, N), written=True)
-        for t, n in ((a.codes, "a.codes"), (w.codes, "w.codes"), (a.scale, "a.scale"), (w.scale, "w.scale"),
-                     (bias, "bias")):
-            _separate(out, t, n, False)
+        _separate_all(out, "out", (a.codes, "a.codes"), (w.codes, "w.codes"), (a.scale, "a.scale"), (w.scale, "w.scale"),
+                      (bias, "bias"))
     _check("veda_int8_matmul", lib().veda_int8_matmul(
         _ptr(a.codes), _ptr(a.scale), _ptr(w.codes), _ptr(w.scale), _ptr(bias), _ptr(out),
         out.stride(0), _DTYPE[out.dtype], M, N, a.K, _stream(stream)))

@@ -364,3 +364,57 @@ def test_overlap_check_against_the_bytes():
             accepted += 1
             assert same is False and not (_bytes_of(views[0]) & _bytes_of(views[1]))
     assert accepted > 500
+
+
+def test_written_buffers_must_not_share_memory(monkeypatch):
+    """Every buffer that a call writes against everything that the call reads or writes besides."""
+    monkeypatch.setattr(veda, "_here", lambda t: True)                   # the checks, on CPU tensors
+    monkeypatch.setattr(veda, "lib", lambda: pytest.fail("the library was reached"))
+    f, bf = torch.float32, torch.bfloat16
+    pool = torch.zeros(1 << 20, dtype=torch.uint8)
+
+    def at(byte, dtype, *shape):
+        n = math.prod(shape) * dtype.itemsize
+        return pool[byte:byte + n].view(dtype).view(shape)
+
+    def refused(call, match):
+        with pytest.raises(ValueError, match=match):
+            call()
+    far = 1 << 19
+    inv = np.ones(8)
+    pos = at(0, torch.int32, 1, 64)
+    refused(lambda: veda.rotary_table(pos, inv, out=at(128, f, 64, 8, 2)), "positions")
+
+    x = at(0, f, 1, 4, 2, 16)
+    table = veda.RotaryTable(at(4096, f, 8, 8, 2), True)
+    rows = at(8192, torch.int32, 1, 4)
+    refused(lambda: veda.rotary(x, table, rows=rows, out=at(8192 - 64, f, 1, 4, 2, 16)), "rows")
+    refused(lambda: veda.rotary(x, table, rows=rows, out=at(4096, f, 1, 4, 2, 16)), "table")
+
+    maps = veda.DeviceMaps(at(65536, torch.int32, 1, 128), at(66560, torch.int32, 1, 1), at(67584, torch.int32, 1, 1),
+                           at(68608, torch.int32, 1), 4, 1, 128)
+    x = at(0, bf, 1, 4, 1, 128)
+    t = veda.RotaryTable(at(4096, f, 4, 64, 2), True)
+    tiles, pooled = at(far, bf, 1, 1, 128, 128), at(131072, f, 1, 1, 1, 3, 128)
+    for given, match in ((dict(out=at(4096, bf, 1, 1, 128, 128)), "table"), (dict(out=at(65536, bf, 1, 1, 128, 128)), "map"),
+                         (dict(out=at(512, bf, 1, 1, 128, 128)), "x"), (dict(pooled=at(512, f, 1, 1, 1, 3, 128)), "x"),
+                         (dict(pooled=at(4096, f, 1, 1, 1, 3, 128)), "table"),
+                         (dict(pooled=at(66560, f, 1, 1, 1, 3, 128)), "valid"),
+                         (dict(pooled=at(far + 16, f, 1, 1, 1, 3, 128)), "out")):
+        refused(lambda: veda.rotary_permute_pool(x, t, maps, **{**dict(out=tiles, pooled=pooled), **given}), match)
+    for place, match in ((4096, "table"), (65536, "map"), (far, "x_t")):
+        refused(lambda: veda.rotary_unpermute(tiles, t, maps, 4, out=at(place, bf, 1, 4, 1, 128)), match)
+
+    x = at(0, bf, 2, 4, 64)
+    w, b, g, sh = (at(4096 + 1024 * i, bf, 2, 64) for i in range(4))
+    for i, n in enumerate(("weight", "bias", "scale", "shift")):
+        refused(lambda: veda.norm_modulate(x, g, sh, w[0], b[0], out=at(4096 + 1024 * i - 512, bf, 2, 4, 64)), n)
+    refused(lambda: veda.norm_gate_add(x, at(far, bf, 2, 4, 64), g, out=at(4096 + 2048 - 512, bf, 2, 4, 64)), "gate")
+    st = veda.NormStats(at(16384, f, 2, 4), at(20480, f, 2, 4))
+    dy = at(far, bf, 2, 4, 64)
+    for place, n in ((4096, "weight"), (5120, "bias"), (6144, "scale"), (16384, "stats.mean"), (20480, "stats.rstd")):
+        refused(lambda: veda.norm_modulate_bwd(dy, x, st, g, w[0], b[0], out=at(place, bf, 2, 4, 64)), n)
+
+    x = at(0, bf, 4, 32)
+    refused(lambda: veda.quantize_int8(x, out=veda.Int8Rows(at(far, torch.int8, 4, 32), at(64, f, 4), 32)), "x")
+    refused(lambda: veda.quantize_int8(x, out=veda.Int8Rows(at(far, torch.int8, 4, 32), at(far + 16, f, 4), 32)), "codes")
