@@ -179,6 +179,12 @@ def _need_maps(maps: "DeviceMaps", H: int, Npad: int, cuda: bool = True) -> None
     _need(maps.nT_per_head, torch.int32, "nT_per_head", cuda, shape=(H,))
 
 
+def _need_tokens(maps: "DeviceMaps", N: int) -> None:
+    """A buffer made for N raster tokens is written where the map has a token and nowhere else."""
+    if N != maps.N:
+        raise ValueError(f"the tile map has {maps.N} tokens, the call {N}")
+
+
 def _need_lists(lists: "BlockLists", B: int, H: int, nT: int, name: str = "lists", cuda: bool = True) -> None:
     """Block lists of a [B, H, nT] problem: counts [B, H, nT], indices [B, H, nT, stride]."""
     if not 0 < lists.stride <= nT:
@@ -888,7 +894,8 @@ def rotary_permute_pool(x: torch.Tensor, table: RotaryTable, maps: DeviceMaps, o
 def rotary_unpermute(x_t: torch.Tensor, table: RotaryTable, maps: DeviceMaps, N: int, inverse: bool = True,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """veda_rotary_unpermute: tiles back to raster order through the transposed rotation -- dQ / dK
-    of the attention's backward to the gradients of the unturned Q / K."""
+    of the attention's backward to the gradients of the unturned Q / K. Tokens that the tile map does not
+    have stay as they are in ``out``; without it, N is the map's."""
     _need(x_t, torch.bfloat16, "x_t")
     if x_t.dim() != 4:
         raise ValueError("x_t: expected shape [B, H, Npad, 128]")
@@ -896,6 +903,7 @@ def rotary_unpermute(x_t: torch.Tensor, table: RotaryTable, maps: DeviceMaps, N:
     _need_maps(maps, H, Npad)
     table._check()
     if out is None:
+        _need_tokens(maps, N)
         out = _new(x_t, (B, N, H, D), torch.bfloat16, stream)
     else:
         _need(out, torch.bfloat16, "out", shape=(B, N, H, D))
@@ -1344,6 +1352,7 @@ def attention_block(x: torch.Tensor, w: BlockWeights, scale: Optional[torch.Tens
     if x.dim() != 3:
         raise ValueError("x: expected shape [B, N, C]")
     B, N, C = x.shape
+    _need_tokens(maps, N)
     H = w.pred_q.shape[0]
     for r, n in ((w.q, "q"), (w.k, "k"), (w.v, "v")):
         if r.rows != H * 128:

@@ -418,3 +418,19 @@ def test_written_buffers_must_not_share_memory(monkeypatch):
     x = at(0, bf, 4, 32)
     refused(lambda: veda.quantize_int8(x, out=veda.Int8Rows(at(far, torch.int8, 4, 32), at(64, f, 4), 32)), "x")
     refused(lambda: veda.quantize_int8(x, out=veda.Int8Rows(at(far, torch.int8, 4, 32), at(far + 16, f, 4), 32)), "codes")
+
+
+def test_token_count_of_the_tile_map(L, monkeypatch):
+    """Tokens that the tile map does not have would come back as whatever their memory held."""
+    monkeypatch.setattr(veda, "_here", lambda t: True)
+    maps = veda.build_tile_map((2, 8, 16), [(1, 8, 16)]).to("cpu")
+    monkeypatch.setattr(veda, "lib", lambda: pytest.fail("the library was reached"))
+    table = lambda n: veda.RotaryTable(torch.ones(n, 64, 2), True)
+    tiles = torch.zeros(1, 1, 256, 128, dtype=torch.bfloat16)
+    for n in (255, 257):
+        with pytest.raises(ValueError, match="tile map has 256 tokens"):
+            veda.rotary_unpermute(tiles, table(n), maps, n)
+        rows = veda.Int8Rows(torch.zeros(128, 64, dtype=torch.int8), torch.ones(128), 64)
+        w = veda.BlockWeights(rows, rows, rows, rows, torch.zeros(1, 128, 384), torch.zeros(1, 128, 384))
+        with pytest.raises(ValueError, match="tile map has 256 tokens"):
+            veda.attention_block(torch.zeros(1, n, 64), w, None, None, None, table(n), maps, [(1, 10)], 0.1)
