@@ -824,10 +824,16 @@ def rotary_table(positions: torch.Tensor, inv_freq: np.ndarray, axis: Optional[n
         raise ValueError("positions: expected shape [rows] or [axes, rows]")
     _need(positions, torch.int32, "positions")
     inv = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    ax = np.zeros(inv.shape, np.int32) if axis is None else np.ascontiguousarray(axis, dtype=np.int32)
+    ax = np.zeros(inv.shape, np.int32) if axis is None else np.asarray(axis)
     if inv.ndim != 1 or ax.shape != inv.shape:
         raise ValueError("inv_freq / axis: expected equal shapes [P]")
     axes, rows = positions.shape
+    if ax.dtype != np.int32:                       # the library checks the values that it gets
+        if ax.dtype.kind not in "iu":
+            raise TypeError(f"axis: expected integers, got {ax.dtype}")
+        if ax.size and not 0 <= int(ax.min()) <= int(ax.max()) < axes:
+            raise ValueError(f"axis: outside the {axes} axes of positions")
+    ax = np.ascontiguousarray(ax, dtype=np.int32)
     if out is None:
         out = _new(positions, (rows, len(inv), 2), torch.float32, stream)
     else:

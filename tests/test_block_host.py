@@ -434,3 +434,16 @@ def test_token_count_of_the_tile_map(L, monkeypatch):
         w = veda.BlockWeights(rows, rows, rows, rows, torch.zeros(1, 128, 384), torch.zeros(1, 128, 384))
         with pytest.raises(ValueError, match="tile map has 256 tokens"):
             veda.attention_block(torch.zeros(1, n, 64), w, None, None, None, table(n), maps, [(1, 10)], 0.1)
+
+
+def test_axis_is_taken_as_it_is(monkeypatch):
+    """An axis of another type or past 32 bits must not arrive as another axis."""
+    monkeypatch.setattr(veda, "_here", lambda t: True)
+    monkeypatch.setattr(veda, "lib", lambda: pytest.fail("the library was reached"))
+    pos, inv = torch.zeros(2, 4, dtype=torch.int32), np.ones(3)
+    for bad in (np.array([0, 2 ** 32, 1]), np.array([0, -2 ** 32, 1]), np.array([0, 2, 1]), np.array([0, -1, 1])):
+        with pytest.raises(ValueError, match="axis"):
+            veda.rotary_table(pos, inv, bad)
+    for bad in (np.array([0.0, 0.7, 1.0]), np.array([False, True, False])):
+        with pytest.raises(TypeError, match="axis"):
+            veda.rotary_table(pos, inv, bad)
