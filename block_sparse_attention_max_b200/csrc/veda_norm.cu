@@ -159,14 +159,22 @@ veda_status resident(Kernel k, int threads, int bytes, int& per_sm) {
 
 // Slices per sequence: together the CTAs that can run at once (so a CTA keeps its channels'
 // parameters for as many rows as possible), no more than there are rows; in the backward with a few
-// rows each, as every slice also writes two rows of fp32 sums.
+// rows each, as every slice also writes two rows of fp32 sums. A sequence has whole slices, so the
+// count is rounded down or up, whichever takes fewer rows one after the other (waves of CTAs times the
+// rows of one), and up where that is equal: rounded down, some of the SMs' places stay empty, rounded up,
+// a few CTAs may run alone behind the others. Measured on 100 M bf16 values, us down / up: 5,120
+// channels, 3 sequences, with an fp32 residual 176 / 334, backward 154 / 221; 7 sequences, forward 80 /
+// 125; equal counts of rows (150 sequences, backward) 358 / 324.
 constexpr int kMaxPerSmFwd = 8, kMaxPerSmBwd = 4, kMaxSms = 160, kMinRowsBwd = 4;
 veda_status slices_for(Kernel k, const Shape& s, int bytes, int sms, bool bwd, int32_t B, int32_t N, int32_t& slices) {
   int per_sm = 0;
   const veda_status st = resident(k, s.threads, bytes, per_sm);
   if (st != VEDA_OK) return st;
   per_sm = std::max(1, std::min(per_sm, bwd ? kMaxPerSmBwd : kMaxPerSmFwd));
-  const int64_t want = (static_cast<int64_t>(std::min(sms, kMaxSms)) * per_sm + B - 1) / B;
+  const int64_t places = static_cast<int64_t>(std::min(sms, kMaxSms)) * per_sm;
+  const int64_t down = std::max<int64_t>(1, places / B), up = (places + B - 1) / B;
+  const auto waves = [&](int64_t each) { return (each * B + places - 1) / places; };
+  const int64_t want = waves(up) * down <= waves(down) * up ? up : down;
   const int64_t rows = (s.warp ? norm::kWarpsPerCta : 1) * (bwd ? kMinRowsBwd : 1);       // a slice's, at least
   slices = static_cast<int32_t>(std::max<int64_t>(1, std::min(want, N / rows + (bwd ? 0 : N % rows != 0))));
   return VEDA_OK;

@@ -323,6 +323,29 @@ def test_many_sequences(V):
     assert R.worst(g.dweight, ref, b * (B + 60) / 61, torch.float32) <= 1
 
 
+@pytest.mark.parametrize("B,N,C", [(3, 200, 5120), (5, 190, 5120), (7, 400, 1024), (40, 33, 1016), (150, 130, 640),
+                                   (200, 17, 2048), (297, 5, 1023)])
+def test_sequence_counts_that_do_not_divide_the_places(V, B, N, C):
+    """Sequences cut into slices whose counts are rounded down or up: rows as in calls of one sequence
+    (bit for bit: a row's result does not depend on its slice), parameter gradients against 64 bits."""
+    x, dy = _rand(B, N, C, seed=90, dtype=torch.bfloat16), _rand(B, N, C, seed=91, dtype=torch.bfloat16)
+    sc, w, res = _rand(B, C, seed=92), _rand(C, seed=93), _rand(B, N, C, seed=94)
+    y, st = V.norm_modulate(x, sc, sc, w, want_stats=True)
+    h = V.norm_gate_add(x, res, sc, w)
+    g = V.norm_modulate_bwd(dy, x, st, sc, w)
+    for b in (0, B // 2, B - 1):
+        one = slice(b, b + 1)
+        yb, sb = V.norm_modulate(x[one], sc[one], sc[one], w, want_stats=True)
+        assert torch.equal(y[one], yb) and torch.equal(st.rstd[one], sb.rstd)
+        assert torch.equal(h[one], V.norm_gate_add(x[one], res[one], sc[one], w))
+        assert torch.equal(g.dx[one], V.norm_modulate_bwd(dy[one], x[one], sb, sc[one], w).dx)
+    _, _, sums = _backward(dy, x, st.mean.double()[..., None], st.rstd.double()[..., None], "layer", _d(w), None, 1 + _d(sc))
+    assert R.worst(g.dscale, *sums["gain"], torch.float32) <= 1
+    assert R.worst(g.dshift, *sums["shift"], torch.float32) <= 1
+    ref, b = sums["weight"]
+    assert R.worst(g.dweight, ref, b * (N + 60 + B) / (N + 60), torch.float32) <= 1      # the sequences' sums are added up
+
+
 def test_refuses_types_and_shapes(V):
     x, res = _rand(2, 3, 64, dtype=torch.bfloat16), _rand(2, 3, 64)
     with pytest.raises(TypeError, match="float64"):
