@@ -2,6 +2,7 @@
 
 Codes and scales are exact. A product's integer sum is exact; its conversion to fp32, the product of
 the scales and the fused multiply-add are one rounding each, then one rounding to the output type."""
+import numpy as np
 import pytest
 import torch
 
@@ -69,6 +70,28 @@ def test_quantize_borders(V):
     for dt in (torch.bfloat16, torch.float16):
         xb = x.to(dt)
         _check_rows(V.quantize_int8(xb), xb)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_scales_are_the_rounded_quotients(V, dtype):
+    """amax / 127 rounded once to fp32, as IEEE division on the CPU gives it (a product with a rounded
+    1 / 127 is a step off for one row in twenty), for every 16-bit mantissa and many of fp32; a row of two
+    tokens as for the fused product of a few tokens."""
+    dt = TYPES[dtype]
+    if dt == torch.float32:
+        a = 1 + torch.arange(4096, dtype=torch.float64) * 2.0 ** -12 + 3 * 2.0 ** -23
+    else:
+        a = 1 + torch.arange(round(1 / torch.finfo(dt).eps), dtype=torch.float64) * torch.finfo(dt).eps
+    a = torch.cat([a * 2.0 ** e for e in (-9, 0, 7)]).to(dt).to(DEV)
+    x = torch.stack([a, -a / 3, a / 7], 1)
+    scale = torch.from_numpy(a.float().cpu().numpy() / np.float32(127))
+    got = V.quantize_int8(x)
+    assert torch.equal(got.scale.cpu(), scale)
+    _check_rows(got, x)
+    one = V.Int8Rows.from_codes(torch.tensor([[1, 0, 0]], device=DEV, dtype=torch.int8), torch.ones(1, device=DEV))
+    for i in range(0, len(a), 97):
+        y = V.int8_linear(x[i:i + 2], one, out_dtype=torch.float32)                  # code 127 times the scale
+        assert torch.equal(y[:, 0].cpu(), (scale[i:i + 2].double() * 127).float())
 
 
 def test_quantize_special_rows(V):

@@ -143,6 +143,51 @@ def test_channels_behind_the_turned_ones_keep_their_bits(V, layout):
         assert torch.isfinite(y[..., :22]).all()
 
 
+SPECIAL = [float("nan"), float("-inf"), -0.0, float("inf")]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("B,N,H,D,rot", [(2, 40, 3, 64, 22), (1, 600, 17, 64, 24), (1, 9, 2, 33, 18), (3, 5, 1, 96, 30),
+                                         (1, 300, 40, 128, 96)])
+def test_in_place_keeps_the_other_channels(V, dtype, layout, B, N, H, D, rot):
+    """In place only the turned channels' vectors are written, and those may hold others: turned
+    channels as out of place, the others bit for bit, whether table rows are given or not."""
+    bits = torch.int32 if dtype == "fp32" else torch.int16
+    x = _rand(B, N, H, D, seed=30, dtype=TYPES[dtype])
+    x[..., rot:rot + 4] = torch.tensor(SPECIAL, device=DEV)[:min(4, D - rot)]
+    t = _table(V, B * N, rot, layout == "interleaved")
+    rows = torch.randperm(B * N, device=DEV).view(B, N).int()
+    for inverse in (False, True):
+        for r in (None, rows):
+            want = V.rotary(x, t, rows=r, inverse=inverse)
+            z = x.clone()
+            assert V.rotary(z, t, rows=r, inverse=inverse, out=z) is z
+            assert torch.equal(z.view(bits), want.view(bits))
+            assert torch.equal(z[..., rot:].contiguous().view(bits), x[..., rot:].contiguous().view(bits))
+            assert torch.isfinite(z[..., :rot]).all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("H,D,rot", [(3, 64, 22), (40, 128, 96), (2, 33, 18)])
+def test_in_place_row_outside_the_table(V, layout, H, D, rot):
+    """In place too, a token whose row is outside the table becomes zeros, all of its channels."""
+    x = _rand(2, 7, H, D, seed=31, dtype=torch.bfloat16)
+    t = _table(V, 9, rot, layout == "interleaved")
+    rows = torch.arange(14, device=DEV, dtype=torch.int32).view(2, 7) % 9
+    want = V.rotary(x, t, rows=rows)
+    V.check_device_status()
+    for b, n, bad in ((0, 3, 9), (1, 6, -1)):
+        given, z = rows.clone(), x.clone()
+        given[b, n] = bad
+        V.rotary(z, t, rows=given, out=z)
+        with pytest.raises(V.VedaError):
+            V.check_device_status()
+        assert (z[b, n] == 0).all()
+        z[b, n] = want[b, n]
+        assert torch.equal(z, want)
+
+
 def test_gradient_is_the_transpose(V):
     """<R x, g> = <x, R^T g>, and the turn's difference quotient along a direction."""
     x, g = _rand(2, 11, 3, 96, seed=10), _rand(2, 11, 3, 96, seed=11)
