@@ -341,9 +341,11 @@ __device__ __forceinline__ void few_load(const QuantArgs& q, int32_t m, int32_t 
 // 10 KB a CTA and saves the separate launch; M x K is bounded (kFewFused) so that it stays small
 // beside the weights.
 // ------------------------------------------------------------------------------------
-// Products of 5,120 x 5,120 (1,024 x 1,024): 2 tokens 7.7 us (3.2) here, 10.7 (4.3) on the tensor
-// cores (int8_tokens_kernel); 4 tokens 13.4 (3.8) and 10.7 (4.4). The fused form also saves the launch
-// that rounds x (4.4 us), so it takes up to 4.
+// Weights from HBM, us of 5,120 x 5,120 (1,024 x 1,024): 2 tokens 9.3 (3.1) here, 3 tokens 9.7 (4.4) on the
+// tensor cores (int8_tokens_kernel), whose time hardly grows up to 16. The fused form against
+// rounding and product in two launches: 1 token 8.7 / 10.6 (2.6 / 4.3), 2 tokens 12.4 / 13.7 (4.1 / 5.4), 3 tokens
+// 14.2 / 12.4 (4.8 / 6.7), 4 tokens of 4,096 13.3 / 11.2 (5.8 / 6.9): 3 and 4 tokens gain by it up to about
+// 2,000 values and lose above, up to kFewFused, where the call still needs no workspace.
 constexpr int kFewMax = 2, kFewMaxFused = 4;
 constexpr int kSomeMax = 128;
 constexpr int kFewThreads = 256;

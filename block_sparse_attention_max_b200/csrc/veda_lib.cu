@@ -34,6 +34,7 @@ struct DeviceInfo {
   int sms = 0;
   bool attrs_set = false;
   int per_sm_copy = 1, per_sm_unpermute = 1, per_sm_pool = 1, per_sm_permpool = 1;   // resident CTAs per SM
+  int token_clusters[int8::tokens::kMaxSplit + 1] = {};      // clusters of so many CTAs of int8_tokens_kernel, one CTA an SM
 };
 constexpr int kMaxDevices = 64;
 constexpr int kRotaryTileSmem = rotary::kTileBuffers * static_cast<int>(rotary::tile_buffer_bytes(rotary::kTileHeads, 64));
@@ -61,6 +62,24 @@ veda_status fail(veda_status st, const std::string& msg) {
 veda_status cuda_fail(cudaError_t e, const char* what) {
   return fail(VEDA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
+
+// Launch of int8_tokens_kernel: `ctas` CTAs in clusters of `split`.
+struct TokensLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  TokensLaunch(int64_t ctas, int split, cudaStream_t s) {
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(int8::tokens::kThreads);
+    cfg.dynamicSmemBytes = int8::tokens::kSmemBytes;
+    cfg.stream = s;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(split);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  TokensLaunch(const TokensLaunch&) = delete;
+};
 
 // Current device: must be compute capability 10.0 (B200). Sets one-time kernel attributes.
 veda_status current_device(int& sms) {
@@ -151,6 +170,19 @@ veda_status current_device(int& sms) {
         (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_pool, pool_kernel, kPoolThreads, 0)) != cudaSuccess ||
         (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.per_sm_permpool, permute_pool_kernel, kPoolThreads, 0)) != cudaSuccess)
       return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+    // every form of the kernel has the same shared memory and launch bounds; the runtime counts one CTA an
+    // SM for it, although two run there
+    const auto tokens_kernel = int8::tokens::int8_tokens_kernel<__nv_bfloat16, 128>;
+    int counted = 0;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&counted, tokens_kernel, int8::tokens::kThreads,
+                                                           int8::tokens::kSmemBytes)) != cudaSuccess)
+      return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
+    for (int w = 1; w <= int8::tokens::kMaxSplit; ++w) {
+      const TokensLaunch l(w, w, nullptr);
+      if ((e = cudaOccupancyMaxActiveClusters(&d.token_clusters[w], tokens_kernel, &l.cfg)) != cudaSuccess)
+        return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+      d.token_clusters[w] = std::max(1, d.token_clusters[w] / std::max(1, counted));
+    }
     d.per_sm_copy = d.per_sm_copy < 1 ? 1 : d.per_sm_copy;
     d.per_sm_unpermute = d.per_sm_unpermute < 1 ? 1 : d.per_sm_unpermute;
     d.per_sm_pool = d.per_sm_pool < 1 ? 1 : d.per_sm_pool;
@@ -376,19 +408,23 @@ veda_status launch_few(const int8::MatArgs& p, const int8::QuantArgs& q, int sms
 // Small enough for the product to round its tokens itself.
 bool few_fused(int64_t M, int64_t kp) { return M <= int8::kFewMaxFused && M * kp <= int8::kFewFused; }
 
-// Some tokens: the split of K that ends first, from the weights' bytes at an SM's share of the HBM rate
-// (a chunk of 16 KB takes 0.37 us, twice that with two CTAs an SM) and 2.5 us a CTA beside its loads.
+// Some tokens: the split of K that ends first. In units of 10 ns, a chunk of 16 KB of weights takes 37
+// at an SM's share of the HBM rate, twice that where two CTAs share the SM, and a CTA 250 beside its
+// loads. Clusters of 7 and 8 leave SMs of a GPC empty (15 of either take one CTA each on 148 SMs), so how
+// many run at once is asked for, not counted by SMs. Equal costs: the larger split, whose CTAs share
+// SMs and hide one another's set-up. Against every split from 1 to 8 (weights from HBM; us of this choice /
+// the best / the worst): 5,120 x 5,120, 8 tokens 9.9 / 9.9 / 16.5, 128 tokens 13.8 / 13.8 / 23.8; 10,240 x 5,120,
+// 64 tokens 15.1 / 15.1 / 26.9; at most 6% above the best in 55 sizes of 1,024 to 30,720 channels.
 template <typename T>
-veda_status launch_tokens(int8::MatArgs& p, int sms, cudaStream_t s) {
+veda_status launch_tokens(int8::MatArgs& p, cudaStream_t s) {
   const int64_t tiles = (p.N - 1) / 128 + 1;
   const int bn = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
   int split = 1;
-  double best = 1e300;
+  int64_t best = INT64_MAX;
   for (int w = 1; w <= std::min(int8::tokens::kMaxSplit, p.chunks); ++w) {
-    const int64_t ctas = tiles * w, waves = (ctas + 2 * sms - 1) / (2 * sms);
-    const double chunk = ctas > sms ? 0.74 : 0.37;
-    const double cost = waves * ((p.chunks + w - 1) / w * chunk + 2.5);
-    if (cost < best) {
+    const int64_t alone = device_info().token_clusters[w], waves = (tiles + 2 * alone - 1) / (2 * alone);
+    const int64_t cost = waves * ((p.chunks + w - 1) / w * (tiles > alone ? 74 : 37) + 250);
+    if (cost <= best) {
       best = cost;
       split = w;
     }
@@ -398,29 +434,19 @@ veda_status launch_tokens(int8::MatArgs& p, int sms, cudaStream_t s) {
   CUtensorMap mW, mX;
   if ((st = encode_codes(mW, p.w, p.kp, p.N, 128)) != VEDA_OK || (st = encode_codes(mX, p.a, p.kp, p.M, bn)) != VEDA_OK) return st;
   if (tiles * split > INT32_MAX) return fail(VEDA_ERR_UNSUPPORTED, "veda_int8_matmul: too many channels");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-  cfg.blockDim = dim3(int8::tokens::kThreads);
-  cfg.dynamicSmemBytes = int8::tokens::kSmemBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(split);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const TokensLaunch l(tiles * split, split, s);
   auto* k = bn == 16   ? int8::tokens::int8_tokens_kernel<T, 16>
             : bn == 32 ? int8::tokens::int8_tokens_kernel<T, 32>
             : bn == 64 ? int8::tokens::int8_tokens_kernel<T, 64>
                        : int8::tokens::int8_tokens_kernel<T, 128>;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, mW, mX, static_cast<const int8::MatArgs&>(p), static_cast<int32_t>(split));
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, k, mW, mX, static_cast<const int8::MatArgs&>(p), static_cast<int32_t>(split));
   return e == cudaSuccess ? VEDA_OK : cuda_fail(e, "int8_tokens_kernel");
 }
 
 template <typename T>
 veda_status launch_int8(int8::MatArgs& p, int sms, cudaStream_t s) {
   if (p.M <= int8::kFewMax) return launch_few<T, false>(p, int8::QuantArgs{}, sms, s);
-  if (p.M <= int8::kSomeMax) return launch_tokens<T>(p, sms, s);
+  if (p.M <= int8::kSomeMax) return launch_tokens<T>(p, s);
   veda_status st = get_encoder();
   if (st != VEDA_OK) return st;
   // Channels per tile: the width that ends first. A chunk of 128 codes costs a pair the slower of its
