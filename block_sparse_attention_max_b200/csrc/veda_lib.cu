@@ -11,6 +11,7 @@
 #include <string>
 
 #include "../../include/veda.h"
+#define VEDA_STATUS_UNIT      // the status word is this unit's (veda_ptx.cuh)
 #include "k_attn.cuh"
 #include "k_heat.cuh"
 #include "k_bwd.cuh"

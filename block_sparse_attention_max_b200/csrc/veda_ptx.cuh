@@ -21,7 +21,12 @@ enum : uint32_t {
   ST_WAIT_SITE_SHIFT = 8,   // bits 8..15: site code of the first wait that ran out
 };
 
-// Defined here: the whole library is one CUDA translation unit (veda_lib.cu).
+// Defined here, so one translation unit includes this file, veda_lib.cu: a second one would have a
+// status word of its own, which veda_check_device_status does not read. (veda_norm.cu, whose kernels
+// flag nothing, does without it.)
+#ifndef VEDA_STATUS_UNIT
+#error "veda_ptx.cuh belongs to veda_lib.cu alone"
+#endif
 __device__ uint32_t g_status = 0;
 
 __device__ __forceinline__ void flag_status(uint32_t bits) { atomicOr(&g_status, bits); }

@@ -447,3 +447,21 @@ def test_axis_is_taken_as_it_is(monkeypatch):
     for bad in (np.array([0.0, 0.7, 1.0]), np.array([False, True, False])):
         with pytest.raises(TypeError, match="axis"):
             veda.rotary_table(pos, inv, bad)
+
+
+def test_the_status_word_has_one_translation_unit():
+    """Kernels of a second unit that included the device helpers would flag a word that nothing reads."""
+    import os
+    import re
+    from block_sparse_attention_max_b200 import build
+
+    def reaches(name, seen):
+        if name in seen or not os.path.exists(os.path.join(build.CSRC, name)):
+            return set()
+        seen.add(name)
+        text = open(os.path.join(build.CSRC, name)).read()
+        below = re.findall(r'#include "([^"]+)"', text)
+        return {name}.union(*(reaches(n, seen) for n in below))
+    users = [n for n in build.SOURCES if "veda_ptx.cuh" in reaches(n, set())]
+    assert users == ["veda_lib.cu"]
+    assert "#error" in open(os.path.join(build.CSRC, "veda_ptx.cuh")).read().split("g_status")[0]
