@@ -16,12 +16,13 @@
 //   dG_B = w P1_B + b P2_B,  dshift_B = P2_B,  dw = sum_B G_B P1_B,  db = sum_B G_B P2_B.
 //
 // All of it is HBM bound: a row is read once and written once, everything between is registers.
-// A row belongs to a group of threads -- a warp for up to 1,024 channels, a CTA above -- whose
-// thread i owns the 8-channel vectors i, i + threads, ...; it therefore keeps A, S (forward) or
-// A, P1, P2 (backward) of its channels in registers for all the rows of its slice of one
-// sequence. Rows come through a ring of 2 to 4 rows in shared memory that each thread fills
-// for itself with 16-byte asynchronous copies (it reads back only what it copied, so no barrier
-// guards the ring); the only barriers are the row reductions'. Statistics and sums are fp32: the
+// A row belongs to a group of threads -- a warp for up to 1,024 channels (256 where rows have no
+// 16-byte boundaries), a CTA above -- whose thread i owns the 8-channel vectors i, i + threads, ...;
+// it therefore keeps A, S (forward) or A, P1, P2 (backward) of its channels in registers for all the
+// rows of its slice of one sequence. Rows come through a ring of 2 to 4 rows in shared memory that
+// each thread fills for itself, with 16-byte asynchronous copies where rows have those boundaries
+// (it reads back only what it copied, so no barrier guards the ring); the only barriers are the row
+// reductions'. Statistics and sums are fp32: the
 // variance is the mean square of the centred values (two passes over registers, not E[x^2] -
 // mean^2), the sums over tokens are fp32 per slice, then over the slices in a fixed order, so
 // results do not change from run to run.
@@ -200,8 +201,10 @@ struct Own {
 };
 
 // This thread's share of a row of T on its way into its own ring slots (slot stride: `threads`
-// units). Aligned rows go there by asynchronous copies. Other rows have only plain loads: start()
-// issues them into registers, finish() -- a row's work later -- writes the ring.
+// units). Aligned rows go there by asynchronous copies. Other rows are read one channel at a time by plain
+// loads (the smallest asynchronous copy has 4 bytes, which 16-bit rows at an odd channel cannot use; fp32
+// rows, which could, go the same way): start() issues them into registers, finish() -- a row's work
+// later -- writes the ring.
 template <typename T, int NV, typename O>
 struct Fetch {
   static constexpr int U = units_of<T>();
@@ -368,8 +371,9 @@ __device__ __forceinline__ Slice slice_of(const Args& a) {
 }
 
 // ------------------------------------------------------------------------------------
-// Forward. TI: type of x; TO: type of y and of the residual. At least two CTAs share an SM, so that
-// one's barriers hide behind the other's work (64 registers at 512 threads, 128 at 256).
+// Forward. TI: type of x; TO: type of y and of the residual. Registers leave room for two CTAs an SM (64
+// at 512 threads, 128 at 256), so that one's barriers hide behind the other's work; rings of wide fp32
+// rows do not (with a residual one CTA runs from 4,096 channels on, where four rows in flight are worth more).
 // ------------------------------------------------------------------------------------
 template <typename TI, typename TO, int NV, bool kWarp, int kMode, int kFixed>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpsPerCta : NV == 4 ? 256 : kMaxThreads, 2)

@@ -54,7 +54,9 @@ int ring_rows(bool bwd, bool is_aligned, int32_t ti, int32_t to, bool res, int32
 //   above, a CTA: the row sums cost a thread the same whatever it holds, so more vectors a thread
 //     are faster as long as their registers leave two CTAs an SM: forward without a residual 4
 //     (5,120: 78%; 2: 72%), with one 2 (8,192: 93%; 4: 78%), backward 2 (5,120: 80%; 4: 60%).
-// Rows without 16-byte boundaries are fetched with plain loads that stall their warp, so there more
+// Rows without 16-byte boundaries, and all whose channels are no multiple of 8 (also fp32 rows of a
+// multiple of 4, which start on such boundaries: 1,004 channels 81 / 71% forward / backward, 1,024 85 /
+// 80%), are fetched with plain loads that stall their warp, so there more
 // warps with less each are faster: above 256 channels a CTA of 1-vector threads, of 128, 256 or 512
 // (backward of 6,147 rows of 1,023, a warp a row 41 us, 64 threads of 2 vectors 54 us).
 struct Shape {

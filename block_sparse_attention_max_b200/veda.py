@@ -1354,7 +1354,9 @@ def attention_block(x: torch.Tensor, w: BlockWeights, scale: Optional[torch.Tens
 
     ``norm_modulate`` (scale, shift), one ``quantize_int8`` for the three ``int8_matmul`` of Q, K and
     V, ``sparse_attention`` with the rotary positions, ``int8_linear`` back to C channels, and
-    ``norm_gate_add`` (gate, residual). Returns the new stream, of x's type."""
+    ``norm_gate_add`` (gate, residual). Returns the new stream, of x's type. Blocks with other stages (a
+    norm of Q and K before the positions, a bias behind the norm after the block) call the operators
+    themselves."""
     if x.dim() != 3:
         raise ValueError("x: expected shape [B, N, C]")
     B, N, C = x.shape
