@@ -1266,6 +1266,11 @@ class PathBuffers:
     lse: torch.Tensor
     o: torch.Tensor
 
+    def tensors(self) -> List[torch.Tensor]:
+        ls = self.lists
+        return [self.q_t, self.k_t, self.v_t, self.pooled_q, self.pooled_k, self.scores, self.workspace, self.o_t, self.lse,
+                self.o, ls.full_cnt, ls.full_idx, ls.part_cnt, ls.part_idx]
+
     @staticmethod
     def allocate(B: int, N: int, H: int, maps: DeviceMaps, rho, device, stream=None) -> "PathBuffers":
         """Buffers for work on ``stream`` (None: the current one): its memory, and the lists' zeros in
@@ -1273,9 +1278,7 @@ class PathBuffers:
         if stream is not None:
             with torch.cuda.stream(stream):
                 bufs = PathBuffers.allocate(B, N, H, maps, rho, device)
-            ls = bufs.lists
-            for t in (bufs.q_t, bufs.k_t, bufs.v_t, bufs.pooled_q, bufs.pooled_k, bufs.scores, bufs.workspace, bufs.o_t,
-                      bufs.lse, bufs.o, ls.full_cnt, ls.full_idx, ls.part_cnt, ls.part_idx):
+            for t in bufs.tensors():
                 t.record_stream(torch.cuda.current_stream())
             return bufs
         nT, Npad, D = maps.nT, maps.Npad, 128
@@ -1405,6 +1408,14 @@ class HostPipeline:
         # follows comp)
         for st in (self.h2d, self.comp):
             st.wait_stream(torch.cuda.current_stream(device))
+        # and go back to it, when the pipeline is dropped, only behind what its streams do with them
+        copied = [t for i in self.inputs for t in i.values()]
+        read = [maps.tile_map, maps.tile_valid, maps.tile_segment, maps.nT_per_head]
+        read += [] if rotary is None else [rotary.cos_sin]
+        for st, ts in ((self.h2d, copied), (self.comp, copied + self.outputs + self.bufs.tensors() + read),
+                       (self.d2h, self.outputs)):
+            for t in ts:
+                t.record_stream(st)
         ev = lambda: [torch.cuda.Event() for _ in range(depth)]
         self.in_ready, self.in_free, self.out_ready, self.out_free = ev(), ev(), ev(), ev()
         self.n = 0

@@ -278,11 +278,33 @@ def test_host_pipeline_waits_for_the_stream_it_is_made_on(L, monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", _FakeStream)
     monkeypatch.setattr(torch.cuda, "Event", lambda *a, **k: object())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     maps = veda.build_tile_map((2, 8, 16), [(1, 8, 16)]).to("cpu")
     table = veda.RotaryTable(torch.ones(256, 64, 2), True)
     pipe = veda.HostPipeline(1, 256, 1, maps, [(1, 10)], 0.1, "cpu", rotary=table)
     for s in (pipe.h2d, pipe.comp):
         assert s.after == [current]
+
+
+def test_host_pipeline_keeps_its_memory_until_its_streams_are_done(L, monkeypatch):
+    """A pipeline that is dropped before its last clips are done must not give its buffers, the maps or
+    the table back to the current stream while its own streams still use them."""
+    kept = []
+    monkeypatch.setattr(_FakeStream, "made", [])
+    monkeypatch.setattr(torch.cuda, "Stream", _FakeStream)
+    monkeypatch.setattr(torch.cuda, "Event", lambda *a, **k: object())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((id(t), s)))
+    maps = veda.build_tile_map((2, 8, 16), [(1, 8, 16)]).to("cpu")
+    table = veda.RotaryTable(torch.ones(256, 64, 2), True)
+    pipe = veda.HostPipeline(1, 256, 1, maps, [(1, 10)], 0.1, "cpu", rotary=table)
+    b, ls = pipe.bufs, pipe.bufs.lists
+    used = {pipe.comp: [b.q_t, b.k_t, b.v_t, b.pooled_q, b.pooled_k, b.scores, b.workspace, b.o_t, b.lse, ls.full_cnt,
+                        ls.full_idx, ls.part_cnt, ls.part_idx, maps.tile_map, maps.tile_valid, maps.tile_segment,
+                        maps.nT_per_head, table.cos_sin, *pipe.outputs, *(t for i in pipe.inputs for t in i.values())],
+            pipe.h2d: [t for i in pipe.inputs for t in i.values()], pipe.d2h: pipe.outputs}
+    for s, ts in used.items():
+        assert {id(t) for t in ts} <= {i for i, st in kept if st is s}
 
 
 def test_path_buffers_come_from_the_launching_stream(L, monkeypatch):
